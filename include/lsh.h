@@ -74,7 +74,9 @@ typedef enum {
   LSH_ERR_SCRATCH_LIMIT = 7 /* problem too large for the library's built-in scratch array */
 } lsh_status;
 
-typedef enum { LSH_F32 = 0, LSH_BF16 = 1 } lsh_dtype;
+/* LSH_E4M3: 8-bit floating point (4 exponent, 3 mantissa bits, largest number
+ * 448), in the 8-bit entry points only. */
+typedef enum { LSH_F32 = 0, LSH_BF16 = 1, LSH_E4M3 = 2 } lsh_dtype;
 
 typedef struct lsh_shape {
   int32_t B;         /* batch */
@@ -304,6 +306,104 @@ LSH_API lsh_status lsh_rev_backward(const lsh_shape* shape, int32_t d_ff, int32_
                                     const void* b2, float* X1, float* X2, float* dX1, float* dX2,
                                     float* dW1, float* db1, float* dW2, float* db2, void* ws,
                                     size_t ws_bytes, void* stream);
+
+/* The 8-bit feed-forward path of a layer: the norm before a sublayer, the
+ * feed-forward's products in 8-bit floating point, and what training them
+ * needs.  No passage of the pages corresponds to it; it serves the layer that
+ * the feed-forward and the reversible block above belong to.
+ *
+ * An 8-bit matrix [rows, cols] is e4m3 codes, row-major, and fp32 scales, one
+ * for each block of 128 columns of a row ([rows, ceil(cols / 128)], "1 x 128")
+ * or of 128 rows ([ceil(rows / 128), ceil(cols / 128)], "128 x 128"; the last
+ * blocks of either axis may be short).  With m the block's largest magnitude,
+ * 2^-96 at least, its scale is m / 448 and its codes are e4m3(448 v / m),
+ * rounded to nearest even; it stands for code * scale.  A block that holds an
+ * infinity or a NaN stands for NaN throughout.
+ *
+ * All sizes called cols, N, K, d_model and d_ff are multiples of 16
+ * (else LSH_ERR_UNSUPPORTED); numbers of rows, M and tokens are any.  The
+ * kernels run on the current device, which must be the buffers' own.
+ * Every call is asynchronous on `stream`, allocates nothing, keeps nothing
+ * between calls and gives the same bits for the same inputs. */
+
+/* Root-mean-square norm with the residual's addition:
+ *   H = X + R   (rounded to X's type; without R, H is X and must be NULL),
+ *   rstd[t] = 1 / sqrt(mean(H[t]^2) + eps),   Y[t] = H[t] * rstd[t] * w.
+ * X, R, H: [rows, cols], X and H LSH_F32 or LSH_BF16 (x_dtype), R bf16 or X's
+ * type (r_dtype, ignored without R); w: [cols] fp32 or bf16 (w_dtype); Y:
+ * [rows, cols] fp32, bf16, or LSH_E4M3 with 1 x 128 scales in `scales` (else
+ * ignored); rstd: [rows] fp32 or NULL.  H may be X itself.  The sum of squares
+ * and the scaling are fp32.  Supported: cols up to 16384; eps > 0. */
+LSH_API lsh_status lsh_rmsnorm_forward(int32_t rows, int32_t cols, int32_t x_dtype,
+                                       int32_t r_dtype, int32_t w_dtype, int32_t y_dtype,
+                                       const void* X, const void* R, const void* w, float eps,
+                                       void* H, void* Y, float* scales, float* rstd,
+                                       void* stream);
+
+/* Gradients of the norm.  With n = H rstd and g = w dY,
+ *   dX[t] = rstd (g - n mean(g n)) + dH[t],   dw = sum_t dY[t] n[t].
+ * dY: [rows, cols] fp32 or bf16 (dy_dtype); H (as normalised), dH (the
+ * gradient that reaches the sum past the norm, or NULL) and dX: x_dtype; dX is
+ * the gradient of X and of R alike, and may be dH itself; dw: [cols] fp32.  ws: at least
+ * lsh_rmsnorm_bwd_ws_size() bytes of device scratch (0 where none is needed). */
+LSH_API size_t lsh_rmsnorm_bwd_ws_size(int32_t rows, int32_t cols);
+LSH_API lsh_status lsh_rmsnorm_backward(int32_t rows, int32_t cols, int32_t x_dtype,
+                                        int32_t dy_dtype, int32_t w_dtype, const void* dY,
+                                        const void* H, const void* w, const float* rstd,
+                                        const void* dH, void* dX, float* dw, void* ws,
+                                        size_t ws_bytes, void* stream);
+
+/* Puts X [rows, cols] (fp32 or bf16) into 8 bits, with 1 x 128 (block_rows 1)
+ * or 128 x 128 blocks (block_rows 128): Y [rows, cols] with `scales`, and Yt,
+ * the 8-bit form of X's transpose, [cols, rows rounded up to a multiple of 16]
+ * with scales_t, the added columns zero.  With 128 x 128 blocks both hold the
+ * same values; with 1 x 128 blocks Yt is blocked along X's rows.  Y or Yt may
+ * be NULL (with its scales). */
+LSH_API lsh_status lsh_quantize_fp8(int32_t rows, int32_t cols, int32_t x_dtype,
+                                    int32_t block_rows, const void* X, void* Y, float* scales,
+                                    void* Yt, float* scales_t, void* stream);
+
+/* C = A B^T + bias, then max(0, .) if relu: A [M, K] with 1 x 128 scales, B
+ * [N, K] with 1 x 128 or 128 x 128 scales (b_block_rows), bias [N] bf16 or
+ * NULL, C [M, N] fp32 or bf16 (c_dtype).  Products and sums are fp32; a
+ * block's sum over K enters the total with its two scales.  ws: at least
+ * lsh_matmul_fp8_ws_size() bytes of device scratch (0 where none is needed). */
+LSH_API size_t lsh_matmul_fp8_ws_size(int32_t M, int32_t N, int32_t K);
+LSH_API lsh_status lsh_matmul_fp8(int32_t M, int32_t N, int32_t K, const void* A,
+                                  const float* a_scales, const void* B, const float* b_scales,
+                                  int32_t b_block_rows, const void* bias, int32_t relu,
+                                  int32_t c_dtype, void* C, void* ws, size_t ws_bytes,
+                                  void* stream);
+
+/* Gradients of C = A B^T + bias (without relu), the quantisers taken as
+ * identities, with every product in 8 bits:
+ *   dA = q(dC) Bt^T,   dB = q(dC^T) q(A^T)^T,   db[n] = sum_m dC[m, n],
+ * q(.) being 1 x 128 blocks.  dC [M, N] and A [M, K] (the values before
+ * quantisation) bf16; Bt [K, N] with 128 x 128 scales, as lsh_quantize_fp8
+ * gives it for B; dA [M, K] fp32 or bf16 (da_dtype); dB [N, K] and db [N]
+ * fp32, overwritten.  Any of dA, dB, db may be NULL (and Bt without dA, A
+ * without dB).  ws: at least lsh_matmul_fp8_bwd_ws_size() bytes. */
+LSH_API size_t lsh_matmul_fp8_bwd_ws_size(int32_t M, int32_t N, int32_t K);
+LSH_API lsh_status lsh_matmul_fp8_backward(int32_t M, int32_t N, int32_t K, const void* dC,
+                                           const void* A, const void* Bt, const float* bt_scales,
+                                           int32_t da_dtype, void* dA, float* dB, float* db,
+                                           void* ws, size_t ws_bytes, void* stream);
+
+/* Chunked feed-forward in 8 bits, forward only (to serve; for gradients see
+ * lsh_ffn_backward and lsh_matmul_fp8_backward):
+ *   Y[t] = W2 q(max(0, W1 X[t] + b1)) + b2,
+ * X [tokens, d_model] with 1 x 128 scales (as lsh_rmsnorm_forward gives it),
+ * W1 [d_ff, d_model] and W2 [d_model, d_ff] with 128 x 128 scales, b1, b2 and
+ * Y bf16; q(.) is 1 x 128 blocks of the fp32 hidden activation.  `chunk`
+ * positions at a time, a multiple of 128, so that the hidden activation exists
+ * for one chunk only (in ws, at least lsh_ffn_fp8_ws_size() bytes); the chunk
+ * does not change the result. */
+LSH_API size_t lsh_ffn_fp8_ws_size(int32_t tokens, int32_t d_model, int32_t d_ff, int32_t chunk);
+LSH_API lsh_status lsh_ffn_forward_fp8(int32_t tokens, int32_t d_model, int32_t d_ff,
+                                       int32_t chunk, const void* X, const float* x_scales,
+                                       const void* W1, const float* w1_scales, const void* b1,
+                                       const void* W2, const float* w2_scales, const void* b2,
+                                       void* Y, void* ws, size_t ws_bytes, void* stream);
 
 /* Test hook for the failure path of the bounded device waits.  No passage of
  * the pages corresponds to it.  Every wait in the kernels gives up after a

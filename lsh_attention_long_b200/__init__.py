@@ -11,3 +11,6 @@ from .lsh import (LshError, Shape, ffn_workspace, forward_host_workspace,  # noq
                   lsh_ffn_backward, lsh_ffn_forward, lsh_forward, lsh_forward_host, lsh_hash, lsh_rev_backward, lsh_rev_forward,
                   lsh_set_wait_test,
                   lsh_sort, lsh_workspace_size, make_shape, rev_workspace, workspace)
+from .fp8 import (ffn_fp8_workspace, lsh_ffn_forward_fp8, lsh_matmul_fp8,  # noqa: F401
+                  lsh_matmul_fp8_backward, lsh_quantize_fp8, lsh_rmsnorm_backward,
+                  lsh_rmsnorm_forward)

@@ -1,0 +1,54 @@
+// e4m3 with a scale per block, shared by the norm, the quantiser and the
+// products.
+//
+// A block (1 x 128 or 128 x 128 entries) with largest magnitude
+// m = max(2^-96, max |v|) is kept as the codes e4m3(448 v / m), rounded to
+// nearest even, and the scale m / 448; it stands for code * scale.  448 is
+// the largest e4m3 number, so a block's largest entry is held without error;
+// the bound 2^-96 keeps both quotients in range and lets a block of zeros be
+// an ordinary block.  An infinity or a NaN makes m infinite or NaN, and every
+// entry of its block then stands for NaN (0 * inf).
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+
+namespace lsh {
+
+constexpr int kQBlock = 128;
+constexpr float kE4m3Max = 448.f;
+constexpr float kMinAmax = 1.2621774483536189e-29f;  // 2^-96
+
+// max(|v|) on the bit patterns: as unsigned integers magnitudes compare like
+// the numbers, and every NaN is above infinity, so one NaN wins the maximum
+__device__ __forceinline__ uint32_t mag_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+__device__ __forceinline__ float block_amax(uint32_t bits) {
+  const uint32_t lo = __float_as_uint(kMinAmax);
+  return __uint_as_float(bits > lo ? bits : lo);
+}
+
+// 448 v / m from inv = 448 / m (rounded): within 2^-22 of the quotient.  For
+// v and m of 8 significant bits (bf16) the quotient is either one of the
+// 5-bit numbers where e4m3 codes border on each other or at least 2^-13 away
+// from all of them: 448 v / m = 7 a / b with integers a, b < 256 up to a
+// power of two, a border is c < 32 up to one, and |7 a 2^u - c b| >= 1 unless
+// equal, so the relative distance is at least 1 / (31 * 255).  Rounding the
+// product to 16 significant bits first (error 2^-17) therefore puts the
+// former exactly on the border, where ties go to even as the definition asks,
+// and leaves the latter on their side.
+template <bool kFromBf16>
+__device__ __forceinline__ float scale_to_e4m3(float v, float inv) {
+  const float p = v * inv;
+  return kFromBf16 ? __uint_as_float((__float_as_uint(p) + 0x80u) & 0xffffff00u) : p;
+}
+
+// Two or four codes, the first in the lowest byte.
+__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  return e4m3x2(a, b) | (e4m3x2(c, d) << 16);
+}
+
+}  // namespace lsh

@@ -1,0 +1,367 @@
+// C ABI of the 8-bit feed-forward path: norm, quantiser, products and the
+// feed-forward made of them.  Included at the end of lsh_api.cu, whose
+// helpers (alignment, launches, tensor maps) it uses.
+#pragma once
+
+namespace {
+
+bool any_misaligned(std::initializer_list<const void*> ps) {
+  for (const void* p : ps)
+    if (misaligned(p)) return true;
+  return false;
+}
+
+bool is_f32_or_bf16(int32_t t) { return t == LSH_F32 || t == LSH_BF16; }
+
+inline int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
+inline size_t kblocks(int cols) { return (size_t)((cols + 127) / 128); }
+// columns of a transposed 8-bit matrix: its K axis, which a product takes in
+// multiples of 16
+inline size_t pitch16(int rows) { return ((size_t)rows + 15) & ~(size_t)15; }
+
+lsh_status norm_check(int32_t rows, int32_t cols) {
+  if (rows < 0 || cols <= 0) return LSH_ERR_INVALID_ARG;
+  if (cols % 16 || cols > lsh::kNormMaxCols) return LSH_ERR_UNSUPPORTED;
+  return LSH_OK;
+}
+
+template <typename XT, int kOut, int kNV, bool kWarp>
+lsh_status norm_fwd_go(const lsh::NormArgs& a, cudaStream_t st) {
+  const long long per = kWarp ? lsh::kNormThreads / 32 : 1;
+  const unsigned grid = (unsigned)((a.rows + per - 1) / per);
+  lsh::rmsnorm_fwd_kernel<XT, kOut, kNV, kWarp><<<grid, lsh::kNormThreads, 0, st>>>(a);
+  return last_launch();
+}
+template <typename XT, int kOut>
+lsh_status norm_fwd_launch(const lsh::NormArgs& a, cudaStream_t st) {
+  if (a.cols <= 256) return norm_fwd_go<XT, kOut, 1, true>(a, st);
+  if (a.cols <= 512) return norm_fwd_go<XT, kOut, 2, true>(a, st);
+  if (a.cols <= 1024) return norm_fwd_go<XT, kOut, 4, true>(a, st);
+  if (a.cols <= 2048) return norm_fwd_go<XT, kOut, 1, false>(a, st);
+  if (a.cols <= 4096) return norm_fwd_go<XT, kOut, 2, false>(a, st);
+  if (a.cols <= 8192) return norm_fwd_go<XT, kOut, 4, false>(a, st);
+  return norm_fwd_go<XT, kOut, 8, false>(a, st);
+}
+template <typename XT>
+lsh_status norm_fwd_launch(const lsh::NormArgs& a, int y_dtype, cudaStream_t st) {
+  if (y_dtype == LSH_E4M3) return norm_fwd_launch<XT, lsh::kNormE4m3>(a, st);
+  if (y_dtype == LSH_BF16) return norm_fwd_launch<XT, lsh::kNormBf16>(a, st);
+  return norm_fwd_launch<XT, lsh::kNormF32>(a, st);
+}
+
+// Blocks of the backward: each leaves one partial row of dw.
+constexpr int kNormBwdBlocks = 592;
+int norm_bwd_blocks(int32_t rows, int32_t cols) {
+  const int per = cols <= lsh::kNormWarpCols ? lsh::kNormThreads / 32 : 1;
+  const int n = ceil_div(rows, per);
+  return n < kNormBwdBlocks ? n : kNormBwdBlocks;
+}
+
+template <typename XT, int kNV, bool kWarp>
+lsh_status norm_bwd_go(const lsh::NormBwdArgs& a, int blocks, cudaStream_t st) {
+  lsh::rmsnorm_bwd_kernel<XT, kNV, kWarp><<<(unsigned)blocks, lsh::kNormThreads, 0, st>>>(a);
+  return last_launch();
+}
+template <typename XT>
+lsh_status norm_bwd_launch(const lsh::NormBwdArgs& a, int blocks, cudaStream_t st) {
+  if (a.cols <= 256) return norm_bwd_go<XT, 1, true>(a, blocks, st);
+  if (a.cols <= 512) return norm_bwd_go<XT, 2, true>(a, blocks, st);
+  if (a.cols <= 1024) return norm_bwd_go<XT, 4, true>(a, blocks, st);
+  if (a.cols <= 2048) return norm_bwd_go<XT, 1, false>(a, blocks, st);
+  if (a.cols <= 4096) return norm_bwd_go<XT, 2, false>(a, blocks, st);
+  if (a.cols <= 8192) return norm_bwd_go<XT, 4, false>(a, blocks, st);
+  return norm_bwd_go<XT, 8, false>(a, blocks, st);
+}
+
+lsh_status column_sum(const float* part, int blocks, int cols, float* out, cudaStream_t st) {
+  lsh::column_sum_kernel<<<(unsigned)ceil_div(cols, 32), 256, 0, st>>>(part, blocks, cols, out);
+  return last_launch();
+}
+
+template <typename XT>
+lsh_status quant_launch(const lsh::QuantArgs& a, int block_rows, cudaStream_t st) {
+  if (block_rows == 1 && !a.yt && !a.colsum) {
+    const long long padded = ((a.cols >> 3) + 15) & ~15;
+    const long long grid = (a.rows * padded + 255) / 256;
+    if (grid > 0x7fffffffLL) return LSH_ERR_UNSUPPORTED;
+    lsh::quant_rows_kernel<XT><<<(unsigned)grid, 256, 0, st>>>(a);
+    return last_launch();
+  }
+  const long long grid = ((a.rows + 127) / 128) * (long long)kblocks(a.cols);
+  if (grid > 0x7fffffffLL) return LSH_ERR_UNSUPPORTED;
+  if (block_rows == 1)
+    lsh::quant_tile_kernel<XT, false><<<(unsigned)grid, 256, 0, st>>>(a);
+  else
+    lsh::quant_tile_kernel<XT, true><<<(unsigned)grid, 256, 0, st>>>(a);
+  return last_launch();
+}
+
+lsh::QuantArgs quant_args(int32_t rows, int32_t cols, const void* X, void* Y, float* scales,
+                          void* Yt, float* scales_t) {
+  lsh::QuantArgs a = {};
+  a.rows = rows; a.cols = cols; a.x = X;
+  a.y = static_cast<uint8_t*>(Y); a.scales = scales;
+  a.yt = static_cast<uint8_t*>(Yt); a.scales_t = scales_t;
+  a.pitch_t = (long long)pitch16(rows);
+  return a;
+}
+
+lsh_status fp8_sizes_check(int32_t M, int32_t N, int32_t K) {
+  if (M < 0 || N <= 0 || K <= 0) return LSH_ERR_INVALID_ARG;
+  if (N % 16 || K % 16) return LSH_ERR_UNSUPPORTED;
+  return LSH_OK;
+}
+
+lsh_status fp8_gemm_launch(const lsh::Fp8GemmArgs& g, cudaStream_t st) {
+  const dim3 grid((unsigned)ceil_div(g.M, 64), (unsigned)ceil_div(g.N, 64));
+  if (grid.y > 65535) return LSH_ERR_UNSUPPORTED;
+  lsh::gemm_fp8_simt_kernel<<<grid, 256, 0, st>>>(g);
+  return last_launch();
+}
+
+lsh::Fp8GemmArgs fp8_gemm_args(int M, int N, int K, const void* A, const float* sa, const void* B,
+                               const float* sb, int b_rows) {
+  lsh::Fp8GemmArgs g = {};
+  g.M = M; g.N = N; g.K = K;
+  g.A = static_cast<const uint8_t*>(A); g.sa = sa;
+  g.B = static_cast<const uint8_t*>(B); g.sb = sb;
+  g.b_rows = b_rows;
+  return g;
+}
+
+// Workspace of lsh_matmul_fp8_backward: dC in 8 bits both ways, A transposed,
+// and the column sums of dC's row blocks.
+struct Fp8BwdLayout {
+  size_t dc, dc_s, dct, dct_s, at, at_s, sums, total;
+};
+Fp8BwdLayout fp8_bwd_layout(int32_t M, int32_t N, int32_t K) {
+  Fp8BwdLayout l;
+  size_t off = 0;
+  auto take = [&](size_t bytes) { const size_t at = off; off += align_up(bytes); return at; };
+  const size_t rb = kblocks(M);
+  l.dc = take((size_t)M * N);
+  l.dc_s = take((size_t)M * kblocks(N) * sizeof(float));
+  l.dct = take((size_t)N * pitch16(M));
+  l.dct_s = take((size_t)N * rb * sizeof(float));
+  l.at = take((size_t)K * pitch16(M));
+  l.at_s = take((size_t)K * rb * sizeof(float));
+  l.sums = take(rb * (size_t)N * sizeof(float));
+  l.total = off;
+  return l;
+}
+
+// Workspace of lsh_ffn_forward_fp8: one chunk's hidden activation.
+struct Ffn8Layout {
+  size_t h, h8, s, total;
+};
+Ffn8Layout ffn8_layout(int32_t rows, int32_t d_ff) {
+  Ffn8Layout l;
+  size_t off = 0;
+  auto take = [&](size_t bytes) { const size_t at = off; off += align_up(bytes); return at; };
+  l.h = take((size_t)rows * d_ff * sizeof(float));
+  l.h8 = take((size_t)rows * d_ff);
+  l.s = take((size_t)rows * kblocks(d_ff) * sizeof(float));
+  l.total = off;
+  return l;
+}
+
+lsh_status ffn8_check(int32_t tokens, int32_t d_model, int32_t d_ff, int32_t chunk) {
+  if (tokens < 0 || d_model <= 0 || d_ff <= 0 || chunk <= 0) return LSH_ERR_INVALID_ARG;
+  if (d_model % 16 || d_ff % 16 || chunk % 128) return LSH_ERR_UNSUPPORTED;
+  return LSH_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+lsh_status lsh_rmsnorm_forward(int32_t rows, int32_t cols, int32_t x_dtype, int32_t r_dtype,
+                               int32_t w_dtype, int32_t y_dtype, const void* X, const void* R,
+                               const void* w, float eps, void* H, void* Y, float* scales,
+                               float* rstd, void* stream) {
+  if (!is_f32_or_bf16(x_dtype) || !is_f32_or_bf16(w_dtype) ||
+      !(is_f32_or_bf16(y_dtype) || y_dtype == LSH_E4M3) || !(eps > 0.f && eps < 1e30f))
+    return LSH_ERR_INVALID_ARG;
+  if (R && !(r_dtype == LSH_BF16 || r_dtype == x_dtype)) return LSH_ERR_INVALID_ARG;
+  const lsh_status s = norm_check(rows, cols);
+  if (s != LSH_OK) return s;
+  if (rows == 0) return LSH_OK;
+  if (!X || !w || !Y || (R && !H) || (!R && H) || (y_dtype == LSH_E4M3 && !scales))
+    return LSH_ERR_INVALID_ARG;
+  if (any_misaligned({X, R, w, H, Y, scales, rstd})) return LSH_ERR_INVALID_ARG;
+  lsh::NormArgs a = {};
+  a.rows = rows; a.cols = cols;
+  a.r_bf16 = r_dtype == LSH_BF16; a.w_bf16 = w_dtype == LSH_BF16;
+  a.x = X; a.r = R; a.w = w; a.eps = eps;
+  a.h = H; a.y = Y; a.scales = scales; a.rstd = rstd;
+  return x_dtype == LSH_BF16 ? norm_fwd_launch<__nv_bfloat16>(a, y_dtype, as_stream(stream))
+                             : norm_fwd_launch<float>(a, y_dtype, as_stream(stream));
+}
+
+size_t lsh_rmsnorm_bwd_ws_size(int32_t rows, int32_t cols) {
+  if (norm_check(rows, cols) != LSH_OK || rows == 0) return 0;
+  const int blocks = norm_bwd_blocks(rows, cols);
+  return blocks > 1 ? align_up((size_t)blocks * cols * sizeof(float)) : 0;
+}
+
+lsh_status lsh_rmsnorm_backward(int32_t rows, int32_t cols, int32_t x_dtype, int32_t dy_dtype,
+                                int32_t w_dtype, const void* dY, const void* H, const void* w,
+                                const float* rstd, const void* dH, void* dX, float* dw, void* ws,
+                                size_t ws_bytes, void* stream) {
+  if (!is_f32_or_bf16(x_dtype) || !is_f32_or_bf16(dy_dtype) || !is_f32_or_bf16(w_dtype))
+    return LSH_ERR_INVALID_ARG;
+  lsh_status s = norm_check(rows, cols);
+  if (s != LSH_OK) return s;
+  if (!dw || misaligned(dw)) return LSH_ERR_INVALID_ARG;
+  cudaStream_t st = as_stream(stream);
+  if (rows == 0)  // a sum of no rows
+    return cudaMemsetAsync(dw, 0, (size_t)cols * sizeof(float), st) == cudaSuccess ? LSH_OK
+                                                                                   : LSH_ERR_CUDA;
+  if (!dY || !H || !w || !rstd || !dX) return LSH_ERR_INVALID_ARG;
+  if (any_misaligned({dY, H, w, rstd, dH, dX, ws})) return LSH_ERR_INVALID_ARG;
+  const size_t need = lsh_rmsnorm_bwd_ws_size(rows, cols);
+  if (need && (!ws || ws_bytes < need)) return LSH_ERR_WORKSPACE;
+  lsh::NormBwdArgs a = {};
+  a.rows = rows; a.cols = cols;
+  a.dy_bf16 = dy_dtype == LSH_BF16; a.w_bf16 = w_dtype == LSH_BF16;
+  a.dy = dY; a.h = H; a.w = w; a.rstd = rstd; a.dh = dH; a.dx = dX;
+  a.dw = need ? static_cast<float*>(ws) : dw;
+  const int blocks = norm_bwd_blocks(rows, cols);
+  s = x_dtype == LSH_BF16 ? norm_bwd_launch<__nv_bfloat16>(a, blocks, st)
+                          : norm_bwd_launch<float>(a, blocks, st);
+  if (s != LSH_OK || !need) return s;
+  return column_sum(a.dw, blocks, cols, dw, st);
+}
+
+lsh_status lsh_quantize_fp8(int32_t rows, int32_t cols, int32_t x_dtype, int32_t block_rows,
+                            const void* X, void* Y, float* scales, void* Yt, float* scales_t,
+                            void* stream) {
+  if (!is_f32_or_bf16(x_dtype) || rows < 0 || cols <= 0 || (block_rows != 1 && block_rows != 128))
+    return LSH_ERR_INVALID_ARG;
+  if (cols % 16) return LSH_ERR_UNSUPPORTED;
+  if (rows == 0) return LSH_OK;
+  if (!X || (!Y && !Yt) || (Y && !scales) || (Yt && !scales_t)) return LSH_ERR_INVALID_ARG;
+  if (any_misaligned({X, Y, scales, Yt, scales_t})) return LSH_ERR_INVALID_ARG;
+  const lsh::QuantArgs a = quant_args(rows, cols, X, Y, scales, Yt, scales_t);
+  return x_dtype == LSH_BF16 ? quant_launch<__nv_bfloat16>(a, block_rows, as_stream(stream))
+                             : quant_launch<float>(a, block_rows, as_stream(stream));
+}
+
+size_t lsh_matmul_fp8_ws_size(int32_t M, int32_t N, int32_t K) {
+  (void)M; (void)N; (void)K;
+  return 0;
+}
+
+lsh_status lsh_matmul_fp8(int32_t M, int32_t N, int32_t K, const void* A, const float* a_scales,
+                          const void* B, const float* b_scales, int32_t b_block_rows,
+                          const void* bias, int32_t relu, int32_t c_dtype, void* C, void* ws,
+                          size_t ws_bytes, void* stream) {
+  if (!is_f32_or_bf16(c_dtype) || (b_block_rows != 1 && b_block_rows != 128))
+    return LSH_ERR_INVALID_ARG;
+  const lsh_status s = fp8_sizes_check(M, N, K);
+  if (s != LSH_OK) return s;
+  if (M == 0) return LSH_OK;
+  if (!A || !a_scales || !B || !b_scales || !C) return LSH_ERR_INVALID_ARG;
+  if (any_misaligned({A, a_scales, B, b_scales, bias, C, ws})) return LSH_ERR_INVALID_ARG;
+  const size_t need = lsh_matmul_fp8_ws_size(M, N, K);
+  if (need && (!ws || ws_bytes < need)) return LSH_ERR_WORKSPACE;
+  lsh::Fp8GemmArgs g = fp8_gemm_args(M, N, K, A, a_scales, B, b_scales, b_block_rows);
+  g.bias = static_cast<const __nv_bfloat16*>(bias);
+  g.relu = relu ? 1 : 0;
+  g.C = C;
+  g.c_f32 = c_dtype == LSH_F32;
+  return fp8_gemm_launch(g, as_stream(stream));
+}
+
+size_t lsh_matmul_fp8_bwd_ws_size(int32_t M, int32_t N, int32_t K) {
+  if (fp8_sizes_check(M, N, K) != LSH_OK || M == 0) return 0;
+  return fp8_bwd_layout(M, N, K).total;
+}
+
+lsh_status lsh_matmul_fp8_backward(int32_t M, int32_t N, int32_t K, const void* dC, const void* A,
+                                   const void* Bt, const float* bt_scales, int32_t da_dtype,
+                                   void* dA, float* dB, float* db, void* ws, size_t ws_bytes,
+                                   void* stream) {
+  if (!is_f32_or_bf16(da_dtype)) return LSH_ERR_INVALID_ARG;
+  lsh_status s = fp8_sizes_check(M, N, K);
+  if (s != LSH_OK) return s;
+  if (any_misaligned({dC, A, Bt, bt_scales, dA, dB, db, ws})) return LSH_ERR_INVALID_ARG;
+  cudaStream_t st = as_stream(stream);
+  if (M == 0) {  // sums of no rows
+    if ((dB && cudaMemsetAsync(dB, 0, (size_t)N * K * sizeof(float), st) != cudaSuccess) ||
+        (db && cudaMemsetAsync(db, 0, (size_t)N * sizeof(float), st) != cudaSuccess))
+      return LSH_ERR_CUDA;
+    return LSH_OK;
+  }
+  if (!dC || (!dA && !dB && !db) || (dA && (!Bt || !bt_scales)) || (dB && !A))
+    return LSH_ERR_INVALID_ARG;
+  const Fp8BwdLayout l = fp8_bwd_layout(M, N, K);
+  if (!ws || ws_bytes < l.total) return LSH_ERR_WORKSPACE;
+  char* w = static_cast<char*>(ws);
+  auto f = [&](size_t at) { return reinterpret_cast<float*>(w + at); };
+  lsh::QuantArgs q = quant_args(M, N, dC, dA ? w + l.dc : nullptr, f(l.dc_s),
+                                dB ? w + l.dct : nullptr, f(l.dct_s));
+  q.colsum = db ? f(l.sums) : nullptr;
+  if ((s = quant_launch<__nv_bfloat16>(q, 1, st)) != LSH_OK) return s;
+  if (db && (s = column_sum(f(l.sums), (int)kblocks(M), N, db, st)) != LSH_OK) return s;
+  if (dA) {
+    lsh::Fp8GemmArgs g = fp8_gemm_args(M, K, N, w + l.dc, f(l.dc_s), Bt, bt_scales, 128);
+    g.C = dA;
+    g.c_f32 = da_dtype == LSH_F32;
+    if ((s = fp8_gemm_launch(g, st)) != LSH_OK) return s;
+  }
+  if (dB) {
+    const lsh::QuantArgs qa = quant_args(M, K, A, nullptr, nullptr, w + l.at, f(l.at_s));
+    if ((s = quant_launch<__nv_bfloat16>(qa, 1, st)) != LSH_OK) return s;
+    lsh::Fp8GemmArgs g = fp8_gemm_args(N, K, (int)pitch16(M), w + l.dct, f(l.dct_s), w + l.at,
+                                       f(l.at_s), 1);
+    g.C = dB;
+    g.c_f32 = 1;
+    if ((s = fp8_gemm_launch(g, st)) != LSH_OK) return s;
+  }
+  return LSH_OK;
+}
+
+size_t lsh_ffn_fp8_ws_size(int32_t tokens, int32_t d_model, int32_t d_ff, int32_t chunk) {
+  if (ffn8_check(tokens, d_model, d_ff, chunk) != LSH_OK || tokens == 0) return 0;
+  return ffn8_layout(tokens < chunk ? tokens : chunk, d_ff).total;
+}
+
+lsh_status lsh_ffn_forward_fp8(int32_t tokens, int32_t d_model, int32_t d_ff, int32_t chunk,
+                               const void* X, const float* x_scales, const void* W1,
+                               const float* w1_scales, const void* b1, const void* W2,
+                               const float* w2_scales, const void* b2, void* Y, void* ws,
+                               size_t ws_bytes, void* stream) {
+  lsh_status s = ffn8_check(tokens, d_model, d_ff, chunk);
+  if (s != LSH_OK) return s;
+  if (tokens == 0) return LSH_OK;
+  if (!X || !x_scales || !W1 || !w1_scales || !b1 || !W2 || !w2_scales || !b2 || !Y)
+    return LSH_ERR_INVALID_ARG;
+  if (any_misaligned({X, x_scales, W1, w1_scales, b1, W2, w2_scales, b2, Y, ws}))
+    return LSH_ERR_INVALID_ARG;
+  const Ffn8Layout l = ffn8_layout(tokens < chunk ? tokens : chunk, d_ff);
+  if (!ws || ws_bytes < l.total) return LSH_ERR_WORKSPACE;
+  cudaStream_t st = as_stream(stream);
+  char* w = static_cast<char*>(ws);
+  float* hs = reinterpret_cast<float*>(w + l.s);
+  for (int64_t c0 = 0; c0 < tokens; c0 += chunk) {
+    const int n = (int)(tokens - c0 < chunk ? tokens - c0 : chunk);
+    lsh::Fp8GemmArgs g1 = fp8_gemm_args(n, d_ff, d_model,
+                                        static_cast<const uint8_t*>(X) + c0 * d_model,
+                                        x_scales + c0 * kblocks(d_model), W1, w1_scales, 128);
+    g1.bias = static_cast<const __nv_bfloat16*>(b1);
+    g1.relu = 1;
+    g1.C = w + l.h;
+    g1.c_f32 = 1;
+    if ((s = fp8_gemm_launch(g1, st)) != LSH_OK) return s;
+    const lsh::QuantArgs q = quant_args(n, d_ff, w + l.h, w + l.h8, hs, nullptr, nullptr);
+    if ((s = quant_launch<float>(q, 1, st)) != LSH_OK) return s;
+    lsh::Fp8GemmArgs g2 = fp8_gemm_args(n, d_model, d_ff, w + l.h8, hs, W2, w2_scales, 128);
+    g2.bias = static_cast<const __nv_bfloat16*>(b2);
+    g2.C = static_cast<__nv_bfloat16*>(Y) + c0 * d_model;
+    if ((s = fp8_gemm_launch(g2, st)) != LSH_OK) return s;
+  }
+  return LSH_OK;
+}
+
+}  // extern "C"

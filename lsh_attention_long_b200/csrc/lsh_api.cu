@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <initializer_list>
 #include <mutex>
 
 #include "attend_bwd_tc.cuh"
@@ -13,8 +14,11 @@
 #include "attend_tc.cuh"
 #include "common.cuh"
 #include "ffn_tc.cuh"
+#include "gemm_fp8.cuh"
 #include "hash_simt.cuh"
 #include "hash_tc.cuh"
+#include "norm.cuh"
+#include "quant.cuh"
 #include "rev.cuh"
 #include "sort.cuh"
 
@@ -1230,3 +1234,5 @@ const char* lsh_status_string(lsh_status status) {
 }
 
 }  // extern "C"
+
+#include "fp8_api.cuh"

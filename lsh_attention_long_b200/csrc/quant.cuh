@@ -1,0 +1,194 @@
+// Quantisation of a matrix into e4m3 blocks of 128 (fp8.cuh), and of its
+// transpose.
+//
+//   quant_rows_kernel   blocks of 1 x 128: eight entries per thread, a block
+//                       in 16 neighbouring lanes;
+//   quant_tile_kernel   a tile of 128 x 128 entries per block of threads, read
+//                       once: blocks of 128 x 128, and for either kind of
+//                       block the transposed matrix, whose columns (the
+//                       positions, the K axis of a weight-gradient product)
+//                       become rows of bytes through shared memory.
+// Both are bound by memory: the input is read once and the codes written.
+#pragma once
+
+#include "fp8.cuh"
+
+namespace lsh {
+
+struct QuantArgs {
+  long long rows;
+  int cols;           // multiple of 16
+  const void* x;      // [rows, cols]
+  uint8_t* y;         // [rows, cols] or NULL
+  float* scales;      // [rows or row blocks, col blocks]
+  uint8_t* yt;        // [cols, pitch_t] or NULL
+  float* scales_t;    // [cols or col blocks, row blocks]
+  long long pitch_t;  // rows rounded up to a multiple of 16; the rest is zero
+  float* colsum;      // [row blocks, cols] sums of the tile's columns, or NULL
+};
+
+template <typename XT>
+__global__ void __launch_bounds__(256) quant_rows_kernel(QuantArgs a) {
+  constexpr bool kBf16 = sizeof(XT) == 2;
+  const int pieces = a.cols >> 3;
+  const int padded = (pieces + 15) & ~15;  // a row starts at lane 0 or 16
+  const long long g = (long long)blockIdx.x * 256 + threadIdx.x;
+  const long long row = g / padded;
+  const int p = (int)(g - row * padded);
+  const bool in = row < a.rows && p < pieces;
+  const size_t at = (size_t)row * a.cols + 8 * p;
+  float v[8];
+  uint32_t m = 0;
+  if (in) {
+    load8(static_cast<const XT*>(a.x) + at, v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = max(m, mag_bits(v[e]));
+  }
+#pragma unroll
+  for (int o = 8; o; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (!in) return;
+  const float am = block_amax(m), inv = kE4m3Max / am;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = scale_to_e4m3<kBf16>(v[e], inv);
+  *reinterpret_cast<uint2*>(a.y + at) =
+      make_uint2(e4m3x4(v[0], v[1], v[2], v[3]), e4m3x4(v[4], v[5], v[6], v[7]));
+  if ((p & 15) == 0) a.scales[(size_t)row * (padded >> 4) + (p >> 4)] = am / kE4m3Max;
+}
+
+// 256 threads; thread (rg, cg) = (tid / 16, tid % 16) holds rows 8 rg .. 8 rg
+// + 7 and columns 8 cg .. 8 cg + 7 of the tile, so a row block (1 x 128) lies
+// in 16 neighbouring lanes and a thread's part of the transposed tile is 8
+// pieces of 8 consecutive bytes.
+template <typename XT, bool kSquare>
+__global__ void __launch_bounds__(256) quant_tile_kernel(QuantArgs a) {
+  constexpr bool kBf16 = sizeof(XT) == 2;
+  __shared__ uint32_t cmax[8][128];
+  __shared__ float csum[8][128];
+  __shared__ float cinv[128];
+  __shared__ __align__(16) uint8_t tile[128 * 128];
+  const int tid = threadIdx.x, warp = tid >> 5, rg = tid >> 4, cg = tid & 15;
+  const int cb = (a.cols + 127) >> 7;
+  const long long tr = blockIdx.x / cb;  // row block
+  const int tc = (int)(blockIdx.x % cb); // column block
+  const long long row0 = tr * 128 + 8 * rg;
+  const int col0 = tc * 128 + 8 * cg;
+  float v[8][8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (row0 + i < a.rows && col0 < a.cols) {
+      load8(static_cast<const XT*>(a.x) + (size_t)(row0 + i) * a.cols + col0, v[i]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[i][e] = 0.f;
+    }
+  }
+  float inv_sq = 0.f;
+  if (kSquare) {  // one maximum for the whole tile
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) m = max(m, mag_bits(v[i][e]));
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if ((tid & 31) == 0) cmax[warp][0] = m;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, cmax[i][0]);
+    const float am = block_amax(m);
+    inv_sq = kE4m3Max / am;
+    if (tid == 0) {
+      const long long rb = (a.rows + 127) >> 7;
+      if (a.y) a.scales[tr * cb + tc] = am / kE4m3Max;
+      if (a.yt) a.scales_t[tc * rb + tr] = am / kE4m3Max;
+    }
+  }
+  if (a.y) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float inv = inv_sq;
+      if (!kSquare) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m = max(m, mag_bits(v[i][e]));
+#pragma unroll
+        for (int o = 8; o; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const float am = block_amax(m);
+        inv = kE4m3Max / am;
+        if (cg == 0 && row0 + i < a.rows)
+          a.scales[(size_t)(row0 + i) * cb + tc] = am / kE4m3Max;
+      }
+      if (row0 + i < a.rows && col0 < a.cols) {
+        float q[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) q[e] = scale_to_e4m3<kBf16>(v[i][e], inv);
+        *reinterpret_cast<uint2*>(a.y + (size_t)(row0 + i) * a.cols + col0) =
+            make_uint2(e4m3x4(q[0], q[1], q[2], q[3]), e4m3x4(q[4], q[5], q[6], q[7]));
+      }
+    }
+  }
+  if (a.colsum) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      float s = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s += v[i][e];
+      s += __shfl_xor_sync(0xffffffffu, s, 16);
+      if ((tid & 16) == 0) csum[warp][8 * cg + e] = s;
+    }
+    __syncthreads();
+    if (tid < 128 && tc * 128 + tid < a.cols) {
+      float s = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s += csum[i][tid];
+      a.colsum[(size_t)tr * a.cols + tc * 128 + tid] = s;
+    }
+  }
+  if (!a.yt) return;
+  if (!kSquare) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = max(m, mag_bits(v[i][e]));
+      m = max(m, __shfl_xor_sync(0xffffffffu, m, 16));
+      if ((tid & 16) == 0) cmax[warp][8 * cg + e] = m;
+    }
+    __syncthreads();
+    if (tid < 128) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = max(m, cmax[i][tid]);
+      const float am = block_amax(m);
+      cinv[tid] = kE4m3Max / am;
+      const int c = tc * 128 + tid;
+      if (c < a.cols) a.scales_t[(size_t)c * ((a.rows + 127) >> 7) + tr] = am / kE4m3Max;
+    }
+    __syncthreads();
+  }
+  // row c of the transposed tile: 16 pieces of 8 bytes, piece rg at rg ^ (c >> 3)
+  // so that the 16 lanes of a store (one per column group) hit distinct banks
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int c = 8 * cg + e;
+    const float inv = kSquare ? inv_sq : cinv[c];
+    float q[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = scale_to_e4m3<kBf16>(v[i][e], inv);
+    *reinterpret_cast<uint2*>(tile + c * 128 + ((rg ^ cg) << 3)) =
+        make_uint2(e4m3x4(q[0], q[1], q[2], q[3]), e4m3x4(q[4], q[5], q[6], q[7]));
+  }
+  __syncthreads();
+  // out: 16 lanes write a row's 128 bytes (pitch_t is a multiple of 16, so
+  // its end never cuts a piece)
+  const long long r = tr * 128 + 8 * (tid & 15);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int c = 16 * k + (tid >> 4);
+    if (tc * 128 + c < a.cols && r < a.pitch_t)
+      *reinterpret_cast<uint2*>(a.yt + (size_t)(tc * 128 + c) * a.pitch_t + r) =
+          *reinterpret_cast<const uint2*>(tile + c * 128 + (((tid & 15) ^ (c >> 3)) << 3));
+  }
+}
+
+}  // namespace lsh

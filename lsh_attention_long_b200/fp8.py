@@ -1,0 +1,274 @@
+"""Python binding of the 8-bit feed-forward path of include/lsh.h: the norm
+before a sublayer, e4m3 matrices with a scale per block of 128, their
+products and the feed-forward made of them (argument marshalling only).
+
+An 8-bit matrix is a pair (codes, scales): codes ``torch.float8_e4m3fn``
+[rows, cols], scales fp32 [rows, ceil(cols / 128)] (1 x 128 blocks) or
+[ceil(rows / 128), ceil(cols / 128)] (128 x 128 blocks).
+
+Calls run on the tensors' device, on its current stream or on ``stream`` (what
+a call allocates then belongs to that stream).
+"""
+
+from __future__ import annotations
+
+import contextlib
+from typing import Optional, Tuple
+
+import torch
+
+from . import lsh as _lsh
+from .lsh import LSH_BF16, LSH_F32, LshError, _validate, load_library
+
+LSH_E4M3 = 2
+F8 = torch.float8_e4m3fn
+_CODES = {torch.float32: LSH_F32, torch.bfloat16: LSH_BF16, F8: LSH_E4M3}
+_FLOATS = (torch.float32, torch.bfloat16)
+_HERE = contextlib.nullcontext()
+
+
+def _up(n: int, to: int) -> int:
+    return -(-n // to) * to
+
+
+def _check(specs) -> torch.device:
+    """The device of (name, tensor, shape, dtype) entries, None tensors
+    skipped.  What is wrong is reported by the library's common check, after
+    the entries have been gone through once."""
+    dev = None
+    for name, t, shape, dtype in specs:
+        if t is None:
+            continue
+        if (not isinstance(t, torch.Tensor) or t.shape != shape or t.dtype is not dtype
+                or not t.is_contiguous() or not t.is_cuda
+                or (dev is not None and t.device != dev)):
+            _validate([(n, x, s, d, True) for n, x, s, d in specs])
+        if dev is None:
+            dev = t.device
+    return dev
+
+
+def _matrix(name: str, t, dtypes) -> Tuple[int, int]:
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError(f"{name} must be a [rows, cols] tensor")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected one of "
+                         f"{', '.join(str(d) for d in dtypes)}")
+    return t.shape
+
+
+def _on(dev: torch.device, stream):
+    """The context in which a call allocates and runs: the tensors' device and
+    the stream asked for."""
+    if stream is not None:
+        if stream.device != dev:
+            raise ValueError(f"stream is on {stream.device}, expected {dev}")
+        return torch.cuda.stream(stream)
+    return _HERE if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
+def _go(name: str, *args) -> None:
+    rc = getattr(_lsh._lib or load_library(), name)(
+        *args, torch.cuda.current_stream().cuda_stream)
+    if rc != 0:
+        raise LshError(name, rc)
+
+
+def _p(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _scratch(name: str, sizes, ws, dev):
+    """(workspace, pointer, bytes): the caller's, or one of the size the library asks for."""
+    if ws is None:
+        n = getattr(_lsh._lib or load_library(), name)(*sizes)
+        if n == 0:
+            return None, None, 0
+        ws = torch.empty(n, dtype=torch.uint8, device=dev)
+    elif not isinstance(ws, torch.Tensor) or ws.device != dev or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous tensor on {dev}")
+    return ws, ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def lsh_rmsnorm_forward(X, w, *, R=None, eps: float = 1e-6, out_dtype=None, H=None, Y=None,
+                        scales=None, rstd=None, want_rstd: bool = False, stream=None):
+    """H = X + R (X's type; X itself without R) and Y = H rsqrt(mean(H^2) + eps) w of every row
+    of X [..., cols].  Returns (H, Y, scales, rstd): Y in ``out_dtype`` (X's type by default;
+    ``torch.float8_e4m3fn`` gives 8 bits with 1 x 128 ``scales`` [rows, ceil(cols / 128)], else
+    None), rstd fp32 [rows] where ``rstd`` is given or ``want_rstd`` (the backward needs it)."""
+    if not isinstance(X, torch.Tensor) or X.dim() < 2 or X.dtype not in _FLOATS:
+        raise ValueError("X must be a [..., cols] tensor of float32 or bfloat16")
+    if not isinstance(w, torch.Tensor) or w.dtype not in _FLOATS:
+        raise ValueError("w must be a [cols] tensor of float32 or bfloat16")
+    shape, cols = X.shape, X.shape[-1]
+    rows = X.numel() // cols if cols else 0
+    yt = out_dtype or X.dtype
+    if yt not in _CODES:
+        raise ValueError(f"out_dtype {yt} is not float32, bfloat16 or float8_e4m3fn")
+    rt = X.dtype
+    if R is not None and isinstance(R, torch.Tensor) and R.dtype is torch.bfloat16:
+        rt = torch.bfloat16
+    if R is None and H is not None:
+        raise ValueError("H is written only where R is given")
+    f32 = torch.float32
+    if yt is not F8:
+        scales = None
+    dev = _check((("X", X, shape, X.dtype), ("w", w, (cols,), w.dtype), ("R", R, shape, rt),
+                  ("H", H, shape, X.dtype), ("Y", Y, shape, yt),
+                  ("scales", scales, (rows, _up(cols, 128) // 128), f32),
+                  ("rstd", rstd, (rows,), f32)))
+    with _on(dev, stream):
+        if R is not None and H is None:
+            H = torch.empty_like(X)
+        if Y is None:
+            Y = torch.empty(shape, dtype=yt, device=dev)
+        if yt is F8 and scales is None:
+            scales = torch.empty((rows, _up(cols, 128) // 128), dtype=f32, device=dev)
+        if rstd is None and want_rstd:
+            rstd = torch.empty((rows,), dtype=f32, device=dev)
+        _go("lsh_rmsnorm_forward", rows, cols, _CODES[X.dtype], _CODES[rt], _CODES[w.dtype],
+            _CODES[yt], X.data_ptr(), _p(R), w.data_ptr(), eps, _p(H), Y.data_ptr(), _p(scales),
+            _p(rstd))
+    return X if R is None else H, Y, scales, rstd
+
+
+def lsh_rmsnorm_backward(dY, H, w, rstd, *, dH=None, dX=None, dw=None, ws=None, stream=None):
+    """Gradients of lsh_rmsnorm_forward: (dX in H's type, dw fp32).  H is the sum as normalised,
+    dH the gradient that reaches it past the norm; dX is the gradient of X and of R alike."""
+    if not isinstance(H, torch.Tensor) or H.dim() < 2 or H.dtype not in _FLOATS:
+        raise ValueError("H must be a [..., cols] tensor of float32 or bfloat16")
+    for name, t in (("w", w), ("dY", dY)):
+        if not isinstance(t, torch.Tensor) or t.dtype not in _FLOATS:
+            raise ValueError(f"{name} must be a tensor of float32 or bfloat16")
+    shape, cols, f32 = H.shape, H.shape[-1], torch.float32
+    rows = H.numel() // cols if cols else 0
+    dev = _check((("dY", dY, shape, dY.dtype), ("H", H, shape, H.dtype),
+                  ("w", w, (cols,), w.dtype), ("rstd", rstd, (rows,), f32),
+                  ("dH", dH, shape, H.dtype), ("dX", dX, shape, H.dtype),
+                  ("dw", dw, (cols,), f32)))
+    with _on(dev, stream):
+        if dX is None:
+            dX = torch.empty_like(H)
+        if dw is None:
+            dw = torch.empty((cols,), dtype=f32, device=dev)
+        ws, wp, wn = _scratch("lsh_rmsnorm_bwd_ws_size", (rows, cols), ws, dev)
+        _go("lsh_rmsnorm_backward", rows, cols, _CODES[H.dtype], _CODES[dY.dtype],
+            _CODES[w.dtype], dY.data_ptr(), H.data_ptr(), w.data_ptr(), rstd.data_ptr(), _p(dH),
+            dX.data_ptr(), dw.data_ptr(), wp, wn)
+    return dX, dw
+
+
+def lsh_quantize_fp8(X, *, block_rows: int = 1, transposed: bool = False, Y=None, scales=None,
+                     Yt=None, scales_t=None, stream=None):
+    """X [rows, cols] (fp32 or bf16) in 8 bits: (Y, scales), blocks of ``block_rows`` (1 or 128) x
+    128; with ``transposed`` also (Yt, scales_t), the 8-bit form of X's transpose [cols, rows
+    rounded up to a multiple of 16], its added columns zero."""
+    rows, cols = _matrix("X", X, _FLOATS)
+    if block_rows not in (1, 128):
+        raise ValueError("block_rows must be 1 or 128")
+    br, f32 = block_rows, torch.float32
+    s_shape = (_up(rows, br) // br, _up(cols, 128) // 128)
+    t_shape = (_up(cols, br) // br, _up(rows, 128) // 128)
+    yt_shape = (cols, _up(rows, 16))
+    if not transposed and (Yt is not None or scales_t is not None):
+        raise ValueError("Yt and scales_t are written only with transposed=True")
+    dev = _check((("X", X, (rows, cols), X.dtype), ("Y", Y, (rows, cols), F8),
+                  ("scales", scales, s_shape, f32), ("Yt", Yt, yt_shape, F8),
+                  ("scales_t", scales_t, t_shape, f32)))
+    with _on(dev, stream):
+        if Y is None:
+            Y = torch.empty((rows, cols), dtype=F8, device=dev)
+        if scales is None:
+            scales = torch.empty(s_shape, dtype=f32, device=dev)
+        if transposed:
+            if Yt is None:
+                Yt = torch.empty(yt_shape, dtype=F8, device=dev)
+            if scales_t is None:
+                scales_t = torch.empty(t_shape, dtype=f32, device=dev)
+        _go("lsh_quantize_fp8", rows, cols, _CODES[X.dtype], br, X.data_ptr(), Y.data_ptr(),
+            scales.data_ptr(), _p(Yt), _p(scales_t))
+    return (Y, scales, Yt, scales_t) if transposed else (Y, scales)
+
+
+def lsh_matmul_fp8(A, a_scales, B, b_scales, *, bias=None, relu: bool = False,
+                   out_dtype=torch.bfloat16, C=None, ws=None, stream=None):
+    """C [M, N] = A B^T (+ bias) (max(0, .) if ``relu``) of 8-bit matrices A [M, K] (1 x 128
+    blocks) and B [N, K] (1 x 128 or 128 x 128 blocks, told by b_scales' shape), in fp32 or bf16."""
+    M, K = _matrix("A", A, (F8,))
+    N, Kb = _matrix("B", B, (F8,))
+    if out_dtype not in _FLOATS:
+        raise ValueError(f"out_dtype {out_dtype} is not float32 or bfloat16")
+    kb, f32 = _up(K, 128) // 128, torch.float32
+    square = (_up(N, 128) // 128, kb)
+    rowwise = isinstance(b_scales, torch.Tensor) and N >= 16 and b_scales.shape == (N, kb)
+    dev = _check((("A", A, (M, K), F8), ("a_scales", a_scales, (M, kb), f32),
+                  ("B", B, (N, K), F8),
+                  ("b_scales", b_scales, (N, kb) if rowwise else square, f32),
+                  ("bias", bias, (N,), torch.bfloat16), ("C", C, (M, N), out_dtype)))
+    with _on(dev, stream):
+        if C is None:
+            C = torch.empty((M, N), dtype=out_dtype, device=dev)
+        ws, wp, wn = _scratch("lsh_matmul_fp8_ws_size", (M, N, K), ws, dev)
+        _go("lsh_matmul_fp8", M, N, K, A.data_ptr(), a_scales.data_ptr(), B.data_ptr(),
+            b_scales.data_ptr(), 1 if rowwise else 128, _p(bias), int(relu), _CODES[out_dtype],
+            C.data_ptr(), wp, wn)
+    return C
+
+
+def lsh_matmul_fp8_backward(dC, A, Bt, bt_scales, *, out_dtype=torch.bfloat16, dA=None, dB=None,
+                            db=None, ws=None, stream=None):
+    """Gradients of C = A B^T + bias (without relu), every product in 8 bits: (dA [M, K] in
+    ``out_dtype``, dB [N, K] fp32, db [N] fp32).  dC and A (before quantisation) bf16; Bt [K, N]
+    and bt_scales are B's transpose in 128 x 128 blocks, as lsh_quantize_fp8 gives it."""
+    bf, f32 = torch.bfloat16, torch.float32
+    M, N = _matrix("dC", dC, (bf,))
+    K = _matrix("A", A, (bf,))[1]
+    if out_dtype not in _FLOATS:
+        raise ValueError(f"out_dtype {out_dtype} is not float32 or bfloat16")
+    dev = _check((("dC", dC, (M, N), bf), ("A", A, (M, K), bf), ("Bt", Bt, (K, N), F8),
+                  ("bt_scales", bt_scales, (_up(K, 128) // 128, _up(N, 128) // 128), f32),
+                  ("dA", dA, (M, K), out_dtype), ("dB", dB, (N, K), f32), ("db", db, (N,), f32)))
+    with _on(dev, stream):
+        if dA is None:
+            dA = torch.empty((M, K), dtype=out_dtype, device=dev)
+        if dB is None:
+            dB = torch.empty((N, K), dtype=f32, device=dev)
+        if db is None:
+            db = torch.empty((N,), dtype=f32, device=dev)
+        ws, wp, wn = _scratch("lsh_matmul_fp8_bwd_ws_size", (M, N, K), ws, dev)
+        _go("lsh_matmul_fp8_backward", M, N, K, dC.data_ptr(), A.data_ptr(), Bt.data_ptr(),
+            bt_scales.data_ptr(), _CODES[out_dtype], dA.data_ptr(), dB.data_ptr(), db.data_ptr(),
+            wp, wn)
+    return dA, dB, db
+
+
+def ffn_fp8_workspace(tokens: int, d_model: int, d_ff: int, chunk: int, device) -> torch.Tensor:
+    """Device scratch for lsh_ffn_forward_fp8: one chunk's hidden activation."""
+    n = load_library().lsh_ffn_fp8_ws_size(tokens, d_model, d_ff, chunk)
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
+
+
+def lsh_ffn_forward_fp8(X, x_scales, W1, w1_scales, b1, W2, w2_scales, b2, chunk: int, *, Y=None,
+                        ws=None, stream=None):
+    """Chunked feed-forward in 8 bits: Y = W2 q(max(0, W1 x + b1)) + b2 (bf16) per position of X
+    [..., d_model] (1 x 128 blocks, x_scales [tokens, ceil(d_model / 128)]; W1 [d_ff, d_model] and
+    W2 [d_model, d_ff] in 128 x 128 blocks), `chunk` positions at a time."""
+    if not isinstance(X, torch.Tensor) or X.dim() < 2:
+        raise ValueError("X must be a [..., d_model] tensor")
+    d_model, bf, f32 = X.shape[-1], torch.bfloat16, torch.float32
+    tokens = X.numel() // d_model if d_model else 0
+    d_ff = W1.shape[0] if isinstance(W1, torch.Tensor) and W1.dim() == 2 else -1
+    mb, fb = _up(d_model, 128) // 128, _up(d_ff, 128) // 128
+    dev = _check((("X", X, X.shape, F8), ("x_scales", x_scales, (tokens, mb), f32),
+                  ("W1", W1, (d_ff, d_model), F8), ("w1_scales", w1_scales, (fb, mb), f32),
+                  ("b1", b1, (d_ff,), bf), ("W2", W2, (d_model, d_ff), F8),
+                  ("w2_scales", w2_scales, (mb, fb), f32), ("b2", b2, (d_model,), bf),
+                  ("Y", Y, X.shape, bf)))
+    with _on(dev, stream):
+        if Y is None:
+            Y = torch.empty(X.shape, dtype=bf, device=dev)
+        ws, wp, wn = _scratch("lsh_ffn_fp8_ws_size", (tokens, d_model, d_ff, chunk), ws, dev)
+        _go("lsh_ffn_forward_fp8", tokens, d_model, d_ff, chunk, X.data_ptr(),
+            x_scales.data_ptr(), W1.data_ptr(), w1_scales.data_ptr(), b1.data_ptr(),
+            W2.data_ptr(), w2_scales.data_ptr(), b2.data_ptr(), Y.data_ptr(), wp, wn)
+    return Y

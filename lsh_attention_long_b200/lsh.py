@@ -27,7 +27,11 @@ EXPORTS = ("lsh_workspace_size", "lsh_hash", "lsh_sort", "lsh_attend_fwd", "lsh_
            "lsh_forward", "lsh_forward_host", "lsh_forward_host_ws_size", "lsh_attend_bwd",
            "lsh_device_status", "lsh_status_string", "lsh_attend_fwd_static", "lsh_set_wait_test",
            "lsh_ffn_ws_size", "lsh_ffn_forward", "lsh_ffn_bwd_ws_size", "lsh_ffn_backward",
-           "lsh_rev_ws_size", "lsh_rev_forward", "lsh_rev_backward")
+           "lsh_rev_ws_size", "lsh_rev_forward", "lsh_rev_backward",
+           "lsh_rmsnorm_forward", "lsh_rmsnorm_bwd_ws_size", "lsh_rmsnorm_backward",
+           "lsh_quantize_fp8", "lsh_matmul_fp8_ws_size", "lsh_matmul_fp8",
+           "lsh_matmul_fp8_bwd_ws_size", "lsh_matmul_fp8_backward", "lsh_ffn_fp8_ws_size",
+           "lsh_ffn_forward_fp8")
 
 
 class LshError(RuntimeError):
@@ -54,7 +58,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                            "`python -m lsh_attention_long_b200.build`")
     lib = ctypes.CDLL(path)
     P, S = ctypes.c_void_p, ctypes.POINTER(Shape)
-    sz = ctypes.c_size_t
+    sz, I = ctypes.c_size_t, ctypes.c_int32
     sig = {
         "lsh_workspace_size": ([S], sz),
         "lsh_hash": ([S, P, P, P, P, P], ctypes.c_int),
@@ -77,6 +81,16 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                             ctypes.c_int),
         "lsh_rev_backward": ([S, ctypes.c_int32, ctypes.c_int32] + [P] * 19 + [sz, P],
                              ctypes.c_int),
+        "lsh_rmsnorm_forward": ([I] * 6 + [P] * 3 + [ctypes.c_float] + [P] * 5, ctypes.c_int),
+        "lsh_rmsnorm_bwd_ws_size": ([I] * 2, sz),
+        "lsh_rmsnorm_backward": ([I] * 5 + [P] * 8 + [sz, P], ctypes.c_int),
+        "lsh_quantize_fp8": ([I] * 4 + [P] * 6, ctypes.c_int),
+        "lsh_matmul_fp8_ws_size": ([I] * 3, sz),
+        "lsh_matmul_fp8": ([I] * 3 + [P] * 4 + [I, P, I, I, P, P, sz, P], ctypes.c_int),
+        "lsh_matmul_fp8_bwd_ws_size": ([I] * 3, sz),
+        "lsh_matmul_fp8_backward": ([I] * 3 + [P] * 4 + [I] + [P] * 4 + [sz, P], ctypes.c_int),
+        "lsh_ffn_fp8_ws_size": ([I] * 4, sz),
+        "lsh_ffn_forward_fp8": ([I] * 4 + [P] * 10 + [sz, P], ctypes.c_int),
         "lsh_status_string": ([ctypes.c_int], ctypes.c_char_p),
     }
     for name, (args, res) in sig.items():
