@@ -112,11 +112,59 @@ lsh_status fp8_sizes_check(int32_t M, int32_t N, int32_t K) {
   return LSH_OK;
 }
 
+// Row-major bytes [rows, cols] read in boxes of 128 columns x box_rows rows,
+// 128-byte swizzled; zeros past the ends.
+bool u8_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows) {
+  const EncodeTiled f = encode_tiled();
+  if (!f) return false;
+  const cuuint64_t dims[2] = {cols, rows};
+  const cuuint64_t strides[1] = {cols};
+  const cuuint32_t box[2] = {128, box_rows};
+  const cuuint32_t elem[2] = {1, 1};
+  return f(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, elem,
+           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int kBN, int kEpi, bool kColScale>
+lsh_status fp8_tc_launch(const lsh::Fp8TcArgs& a, cudaStream_t st) {
+  const lsh::Fp8GemmArgs& g = a.g;
+  CUtensorMap ma, mb;
+  if (!u8_map(&ma, g.A, (uint64_t)g.M, (uint64_t)g.K, lsh::kF8BM) ||
+      !u8_map(&mb, g.B, (uint64_t)g.N, (uint64_t)g.K, kBN))
+    return LSH_ERR_CUDA;
+  constexpr size_t smem = lsh::fp8_tc_smem_bytes<kBN, kColScale>();
+  const auto kernel = lsh::gemm_fp8_tc_kernel<kBN, kEpi, kColScale>;
+  const lsh_status s = allow_smem(kernel, smem);
+  if (s != LSH_OK) return s;
+  const long long units = (long long)ceil_div(g.M, lsh::kF8BM) * ceil_div(g.N, kBN);
+  if (units > 0x3fffffff) return LSH_ERR_UNSUPPORTED;
+  const int sms = num_sms();
+  return launch_pdl(kernel, dim3((unsigned)(units < sms ? units : sms)), dim3(lsh::kF8Threads),
+                    smem, st, ma, mb, a);
+}
+
 lsh_status fp8_gemm_launch(const lsh::Fp8GemmArgs& g, cudaStream_t st) {
-  const dim3 grid((unsigned)ceil_div(g.M, 64), (unsigned)ceil_div(g.N, 64));
-  if (grid.y > 65535) return LSH_ERR_UNSUPPORTED;
-  lsh::gemm_fp8_simt_kernel<<<grid, 256, 0, st>>>(g);
-  return last_launch();
+  lsh::Fp8TcArgs a = {};
+  a.g = g;
+  a.wait_limit = g_wait_limit;
+  const long long units = (long long)ceil_div(g.M, lsh::kF8BM) * ceil_div(g.N, 256);
+  const bool wide = units >= num_sms();
+  if (g.b_rows == 1)
+    return wide ? fp8_tc_launch<256, lsh::kF8Store, true>(a, st)
+                : fp8_tc_launch<128, lsh::kF8Store, true>(a, st);
+  return wide ? fp8_tc_launch<256, lsh::kF8Store, false>(a, st)
+              : fp8_tc_launch<128, lsh::kF8Store, false>(a, st);
+}
+
+// The hidden activation of the feed-forward: max(0, A B^T + bias) in 8 bits.
+lsh_status fp8_gemm_quant_launch(const lsh::Fp8GemmArgs& g, void* Q, float* qs, cudaStream_t st) {
+  lsh::Fp8TcArgs a = {};
+  a.g = g;
+  a.Q = static_cast<uint8_t*>(Q);
+  a.qs = qs;
+  a.wait_limit = g_wait_limit;
+  return fp8_tc_launch<256, lsh::kF8Quant, false>(a, st);
 }
 
 lsh::Fp8GemmArgs fp8_gemm_args(int M, int N, int K, const void* A, const float* sa, const void* B,
@@ -152,13 +200,12 @@ Fp8BwdLayout fp8_bwd_layout(int32_t M, int32_t N, int32_t K) {
 
 // Workspace of lsh_ffn_forward_fp8: one chunk's hidden activation.
 struct Ffn8Layout {
-  size_t h, h8, s, total;
+  size_t h8, s, total;
 };
 Ffn8Layout ffn8_layout(int32_t rows, int32_t d_ff) {
   Ffn8Layout l;
   size_t off = 0;
   auto take = [&](size_t bytes) { const size_t at = off; off += align_up(bytes); return at; };
-  l.h = take((size_t)rows * d_ff * sizeof(float));
   l.h8 = take((size_t)rows * d_ff);
   l.s = take((size_t)rows * kblocks(d_ff) * sizeof(float));
   l.total = off;
@@ -350,12 +397,7 @@ lsh_status lsh_ffn_forward_fp8(int32_t tokens, int32_t d_model, int32_t d_ff, in
                                         static_cast<const uint8_t*>(X) + c0 * d_model,
                                         x_scales + c0 * kblocks(d_model), W1, w1_scales, 128);
     g1.bias = static_cast<const __nv_bfloat16*>(b1);
-    g1.relu = 1;
-    g1.C = w + l.h;
-    g1.c_f32 = 1;
-    if ((s = fp8_gemm_launch(g1, st)) != LSH_OK) return s;
-    const lsh::QuantArgs q = quant_args(n, d_ff, w + l.h, w + l.h8, hs, nullptr, nullptr);
-    if ((s = quant_launch<float>(q, 1, st)) != LSH_OK) return s;
+    if ((s = fp8_gemm_quant_launch(g1, w + l.h8, hs, st)) != LSH_OK) return s;
     lsh::Fp8GemmArgs g2 = fp8_gemm_args(n, d_model, d_ff, w + l.h8, hs, W2, w2_scales, 128);
     g2.bias = static_cast<const __nv_bfloat16*>(b2);
     g2.C = static_cast<__nv_bfloat16*>(Y) + c0 * d_model;
