@@ -112,49 +112,66 @@ lsh_status fp8_sizes_check(int32_t M, int32_t N, int32_t K) {
   return LSH_OK;
 }
 
-// Row-major bytes [rows, cols] read in boxes of 128 columns x box_rows rows,
-// 128-byte swizzled; zeros past the ends.
-bool u8_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows) {
+// Row-major matrix [rows, cols] read or written in boxes of 128 bytes x
+// box_rows rows, 128-byte swizzled; zeros past the ends.
+bool map_128b(CUtensorMap* m, CUtensorMapDataType type, uint32_t size, const void* base,
+              uint64_t rows, uint64_t cols, uint32_t box_rows) {
   const EncodeTiled f = encode_tiled();
   if (!f) return false;
   const cuuint64_t dims[2] = {cols, rows};
-  const cuuint64_t strides[1] = {cols};
-  const cuuint32_t box[2] = {128, box_rows};
+  const cuuint64_t strides[1] = {cols * size};
+  const cuuint32_t box[2] = {128 / size, box_rows};
   const cuuint32_t elem[2] = {1, 1};
-  return f(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, elem,
+  return f(m, type, 2, const_cast<void*>(base), dims, strides, box, elem,
            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-
-template <int kBN, int kEpi, bool kColScale>
-lsh_status fp8_tc_launch(const lsh::Fp8TcArgs& a, cudaStream_t st) {
-  const lsh::Fp8GemmArgs& g = a.g;
-  CUtensorMap ma, mb;
-  if (!u8_map(&ma, g.A, (uint64_t)g.M, (uint64_t)g.K, lsh::kF8BM) ||
-      !u8_map(&mb, g.B, (uint64_t)g.N, (uint64_t)g.K, kBN))
-    return LSH_ERR_CUDA;
-  constexpr size_t smem = lsh::fp8_tc_smem_bytes<kBN, kColScale>();
-  const auto kernel = lsh::gemm_fp8_tc_kernel<kBN, kEpi, kColScale>;
-  const lsh_status s = allow_smem(kernel, smem);
-  if (s != LSH_OK) return s;
-  const long long units = (long long)ceil_div(g.M, lsh::kF8BM) * ceil_div(g.N, kBN);
-  if (units > 0x3fffffff) return LSH_ERR_UNSUPPORTED;
-  const int sms = num_sms();
-  return launch_pdl(kernel, dim3((unsigned)(units < sms ? units : sms)), dim3(lsh::kF8Threads),
-                    smem, st, ma, mb, a);
+bool u8_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows) {
+  return map_128b(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, base, rows, cols, box_rows);
 }
 
+template <int kPair, int kBN, int kEpi, bool kColScale>
+lsh_status fp8_tc_launch(const lsh::Fp8TcArgs& a, cudaStream_t st) {
+  const lsh::Fp8GemmArgs& g = a.g;
+  CUtensorMap ma, mb, mc;
+  if (!u8_map(&ma, g.A, (uint64_t)g.M, (uint64_t)g.K, lsh::kF8BM) ||
+      !u8_map(&mb, g.B, (uint64_t)g.N, (uint64_t)g.K, kBN / kPair))
+    return LSH_ERR_CUDA;
+  const uint64_t M = (uint64_t)g.M, N = (uint64_t)g.N;
+  if (!(kEpi == lsh::kF8Quant ? u8_map(&mc, a.Q, M, N, 32)
+        : g.c_f32 ? map_128b(&mc, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, g.C, M, N, 32)
+                  : map_128b(&mc, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, g.C, M, N, 32)))
+    return LSH_ERR_CUDA;
+  constexpr size_t smem = lsh::fp8_tc_smem_bytes<kPair, kBN, kEpi, kColScale>();
+  const auto kernel = lsh::gemm_fp8_tc_kernel<kPair, kBN, kEpi, kColScale>;
+  // the kernel's register split adds up only if it was built with kF8Regs
+  static const bool regs_ok = [&] {
+    cudaFuncAttributes at;
+    return cudaFuncGetAttributes(&at, kernel) == cudaSuccess && at.numRegs == lsh::kF8Regs;
+  }();
+  if (!regs_ok) return LSH_ERR_CUDA;
+  const lsh_status s = allow_smem(kernel, smem);
+  if (s != LSH_OK) return s;
+  const long long units = (long long)ceil_div(g.M, kPair * lsh::kF8BM) * ceil_div(g.N, kBN);
+  if (units > 0x3fffffff) return LSH_ERR_UNSUPPORTED;
+  const int fit = num_sms() / kPair;
+  return launch_pdl_cluster(kernel, dim3((unsigned)((units < fit ? units : fit) * kPair)),
+                    dim3(lsh::kF8Threads), smem, st, kPair, ma, mb, mc, a);
+}
+
+// Tiles: a pair of CTAs on 256 x 256 once those alone give every other SM one
+// (a lone tile of 128 x 128 needs twice the loads per product), else 128 x 128.
 lsh_status fp8_gemm_launch(const lsh::Fp8GemmArgs& g, cudaStream_t st) {
   lsh::Fp8TcArgs a = {};
   a.g = g;
   a.wait_limit = g_wait_limit;
-  const long long units = (long long)ceil_div(g.M, lsh::kF8BM) * ceil_div(g.N, 256);
-  const bool wide = units >= num_sms();
+  const long long units = (long long)ceil_div(g.M, 256) * ceil_div(g.N, 256);
+  const bool pair = units * 4 >= num_sms();
   if (g.b_rows == 1)
-    return wide ? fp8_tc_launch<256, lsh::kF8Store, true>(a, st)
-                : fp8_tc_launch<128, lsh::kF8Store, true>(a, st);
-  return wide ? fp8_tc_launch<256, lsh::kF8Store, false>(a, st)
-              : fp8_tc_launch<128, lsh::kF8Store, false>(a, st);
+    return pair ? fp8_tc_launch<2, 256, lsh::kF8Store, true>(a, st)
+                : fp8_tc_launch<1, 128, lsh::kF8Store, true>(a, st);
+  return pair ? fp8_tc_launch<2, 256, lsh::kF8Store, false>(a, st)
+              : fp8_tc_launch<1, 128, lsh::kF8Store, false>(a, st);
 }
 
 // The hidden activation of the feed-forward: max(0, A B^T + bias) in 8 bits.
@@ -164,7 +181,9 @@ lsh_status fp8_gemm_quant_launch(const lsh::Fp8GemmArgs& g, void* Q, float* qs, 
   a.Q = static_cast<uint8_t*>(Q);
   a.qs = qs;
   a.wait_limit = g_wait_limit;
-  return fp8_tc_launch<256, lsh::kF8Quant, false>(a, st);
+  const long long units = (long long)ceil_div(g.M, 256) * ceil_div(g.N, 256);
+  return units * 4 >= num_sms() ? fp8_tc_launch<2, 256, lsh::kF8Quant, false>(a, st)
+                                : fp8_tc_launch<1, 256, lsh::kF8Quant, false>(a, st);
 }
 
 lsh::Fp8GemmArgs fp8_gemm_args(int M, int N, int K, const void* A, const float* sa, const void* B,

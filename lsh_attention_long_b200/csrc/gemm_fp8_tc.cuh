@@ -5,17 +5,29 @@
 // own: four tcgen05.mma of K = 32, the first overwriting, go into one of the
 // 512 / kBN tensor-memory buffers, and the epilogue warps read it back and
 // add it, times sa[m, kb] sb[n, kb], to their fp32 totals in registers.  A
-// 128 x 256 tile's block is 512 cycles of tensor-core time; reading it back
-// and one FMA per entry are 256 cycles each of what an SM's four schedulers
-// can do in that time, so both fit beside it.
+// 128 x 256 tile's block is 512 cycles of an SM's tensor core; reading it back
+// is 256 cycles of tensor memory and one packed FMA per two entries 128 of
+// each scheduler's, so both fit beside it.
 //
-// Warp roles (320 threads, persistent blocks, one per SM):
-//   warp 0     one thread loads A (128 rows) and B (kBN rows) tiles of 128
-//              bytes with TMA (128-byte swizzle; zeros past the matrices'
-//              ends) into a ring of kStages stages;
-//   warp 1     one thread issues the tcgen05.mma;
-//   warps 2-9  two warpgroups, one for each half of the tile's columns; a
-//              thread has one row (its TMEM lane) and kBN / 2 totals.
+// kPair 2: two CTAs (a cluster) work on a 256 x 256 tile with pair MMAs.  Each
+// loads its own 128 rows of A and half of B's, 32 KB per block of K in place
+// of the 48 KB of a 128 x 256 tile alone, which the path from L2 would bound.
+// kPair 1 serves products with few tiles.
+//
+// Warp roles (384 threads, persistent blocks, one per SM):
+//   warp 0      one thread loads A and B tiles of 128-byte rows with TMA
+//               (128-byte swizzle; zeros past the matrices' ends) into a ring
+//               of kStages stages;
+//   warps 1, 2  one lane each (of the pair's even rank) issues the tcgen05.mma
+//               of every other block: the waits, four MMAs and two commits of
+//               a block are some 680 cycles of one thread's time, more than
+//               the 512 that the MMAs take;
+//   warp 3      brings the scales: rows of sa (and, b_rows 1, of sb) lie n_k
+//               apart, so a warp's load of one block's column touches 32 lines;
+//               here each is loaded once, some blocks ahead, and reaches the
+//               epilogue through a ring in shared memory;
+//   warps 4-11  two warpgroups, one for each half of the tile's columns; a
+//               thread has one row (its TMEM lane) and kBN / 2 totals.
 #pragma once
 
 #include <cuda.h>
@@ -26,8 +38,14 @@
 
 namespace lsh {
 
-constexpr int kF8Threads = 320;
+constexpr int kF8Threads = 384;
+// Registers: 168 a thread at launch (what 384 threads can have), of which the
+// first warpgroup gives up 96, and each epilogue thread gets 48 more.
+constexpr int kF8Regs = 168, kF8RegsLow = 72, kF8RegsHigh = 216;
+static_assert(128 * kF8RegsLow + 256 * kF8RegsHigh == kF8Threads * kF8Regs, "register split");
 constexpr int kF8BM = 128, kF8BK = 128;
+
+constexpr int kF8Slots = 2;  // ring of scales, in four blocks of K
 
 enum Fp8Epi { kF8Store = 0, kF8Quant = 1 };
 
@@ -38,35 +56,53 @@ struct Fp8TcArgs {
   long long wait_limit;
 };
 
-template <int kBN, bool kColScale>
+template <int kPair, int kBN, int kEpi, bool kColScale>
 struct Fp8Cfg {
-  static constexpr int kStages = kBN == 128 ? 6 : kColScale ? 3 : 4;  // what 227 KB hold
-  static constexpr int kABytes = kF8BM * kF8BK, kBBytes = kBN * kF8BK;
+  static constexpr int kCols = kBN / 2;  // columns of an epilogue thread
+  static constexpr int kABytes = kF8BM * kF8BK, kBBytes = kBN / kPair * kF8BK;
   static constexpr int kBufs = 512 / kBN;
-  static constexpr int kOutBytes = 8 * 32 * 128;  // a staging row of 128 B per epilogue thread
+  // staging of an epilogue warp: 32 rows of its columns in bf16 or e4m3 (fp32
+  // leaves in two parts), as boxes of 32 rows of 128 bytes
+  static constexpr int kOutBoxes = kEpi == kF8Quant ? 1 : kCols / 64;
+  static constexpr int kOutBytes = 8 * kOutBoxes * 4096;
+  static constexpr int kScaleBytes =
+      kF8Slots * 4 * 4 * (kColScale ? kF8BM + kBN : 2 * kF8BM);
+  static constexpr int kStages =  // what is left of 227 KB, less alignment and barriers
+      (232448 - 1024 - 512 - kOutBytes - kScaleBytes) / (kABytes + kBBytes);
 };
 
-template <int kBN, bool kColScale>
+template <int kPair, int kBN, int kEpi, bool kColScale>
 struct Fp8Smem {
-  using C = Fp8Cfg<kBN, kColScale>;
-  // b_rows 1: a block's column scales, by parity and column
-  float sb[2][kColScale ? kBN : 4];
+  using C = Fp8Cfg<kPair, kBN, kEpi, kColScale>;
+  // scales of the blocks to come, four to a slot: per half of the columns and
+  // row sa * sb, or (b_rows 1) per row sa and per column sb
+  float4 rs[kF8Slots][kColScale ? 1 : 2][kF8BM];
+  float cs[kColScale ? kF8Slots : 1][4][kColScale ? kBN : 1];
   uint64_t full[C::kStages], empty[C::kStages];
   uint64_t acc_full[C::kBufs], acc_empty[C::kBufs];
-  uint64_t mma_done;
+  uint64_t sc_full[kF8Slots], sc_empty[kF8Slots];
+  uint64_t mma_done[2];
   uint32_t tmem_base;
   int abort;
 };
 
-template <int kBN, bool kColScale>
+template <int kPair, int kBN, int kEpi, bool kColScale>
 __host__ __device__ constexpr size_t fp8_tc_smem_bytes() {
-  using C = Fp8Cfg<kBN, kColScale>;
-  return 1024 + (size_t)C::kStages * (C::kABytes + C::kBBytes) + C::kOutBytes +
-         sizeof(Fp8Smem<kBN, kColScale>);
+  using C = Fp8Cfg<kPair, kBN, kEpi, kColScale>;
+  constexpr size_t bytes = 1024 + (size_t)C::kStages * (C::kABytes + C::kBBytes) + C::kOutBytes +
+                           sizeof(Fp8Smem<kPair, kBN, kEpi, kColScale>);
+  static_assert(bytes <= 232448 && C::kStages >= 3, "shared memory of a block");
+  return bytes;
 }
-static_assert(fp8_tc_smem_bytes<256, false>() <= 232448 && fp8_tc_smem_bytes<256, true>() <= 232448 &&
-                  fp8_tc_smem_bytes<128, true>() <= 232448,
-              "shared memory of a block");
+
+constexpr int kChunk = 16;  // columns read back at a time
+
+// Waits for a phase unless the CTA aborted; false on abort or timeout.  The
+// clock is read only where the first look finds nothing.
+__device__ __forceinline__ bool f8_wait(uint64_t* bar, uint32_t parity, int* abort,
+                                        long long limit) {
+  return tc::mbar_test(bar, parity) || gm_wait(bar, parity, abort, limit);
+}
 
 // OR of pred over the 256 epilogue threads (named barrier 3).
 __device__ __forceinline__ bool f8_any(bool pred) {
@@ -82,15 +118,16 @@ __device__ __forceinline__ bool f8_any(bool pred) {
   return r != 0;
 }
 
-template <int kBN, int kEpi, bool kColScale>
+template <int kPair, int kBN, int kEpi, bool kColScale>
 __global__ void __launch_bounds__(kF8Threads, 1)
     gemm_fp8_tc_kernel(const __grid_constant__ CUtensorMap map_a,
-                       const __grid_constant__ CUtensorMap map_b, Fp8TcArgs a) {
-  using C = Fp8Cfg<kBN, kColScale>;
-  using Smem = Fp8Smem<kBN, kColScale>;
+                       const __grid_constant__ CUtensorMap map_b,
+                       const __grid_constant__ CUtensorMap map_c, Fp8TcArgs a) {
+  using C = Fp8Cfg<kPair, kBN, kEpi, kColScale>;
+  using Smem = Fp8Smem<kPair, kBN, kEpi, kColScale>;
   static_assert(kEpi != kF8Quant || kBN == 256, "a thread's columns are one block");
   constexpr int kStages = C::kStages, kBufs = C::kBufs;
-  constexpr int kCols = kBN / 2;  // columns of an epilogue thread
+  constexpr int kCols = C::kCols;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = tc::smem_u32(smem_raw);
   uint8_t* sm = smem_raw + (((raw + 1023u) & ~1023u) - raw);
@@ -101,6 +138,8 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   const Fp8GemmArgs& g = a.g;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const long long limit = a.wait_limit;
+  const int rank = kPair == 2 ? (int)tc::cluster_rank() : 0;
+  const int first_unit = blockIdx.x / kPair, unit_step = gridDim.x / kPair;
 
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -109,42 +148,77 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     }
     for (int b = 0; b < kBufs; ++b) {
       tc::mbar_init(&S.acc_full[b], 1);
-      tc::mbar_init(&S.acc_empty[b], 256);
+      tc::mbar_init(&S.acc_empty[b], 8 * kPair);  // one arrival per epilogue warp
     }
-    tc::mbar_init(&S.mma_done, 1);
+    for (int b = 0; b < kF8Slots; ++b) {
+      tc::mbar_init(&S.sc_full[b], 1);
+      tc::mbar_init(&S.sc_empty[b], 8);
+    }
+    tc::mbar_init(&S.mma_done[0], 1);
+    tc::mbar_init(&S.mma_done[1], 1);
     tc::mbar_init_fence();
     S.abort = 0;
   }
   if (warp == 1) {
-    tc::tmem_alloc(&S.tmem_base, 512);
-    tc::tmem_relinquish();
+    if (kPair == 2) {
+      tc::tmem_alloc_pair(&S.tmem_base, 512);
+      tc::tmem_relinquish_pair();
+    } else {
+      tc::tmem_alloc(&S.tmem_base, 512);
+      tc::tmem_relinquish();
+    }
   }
   tc::fence_before_sync();
-  __syncthreads();
+  if (kPair == 2)
+    tc::cluster_sync();  // the peer's barriers are set up too
+  else
+    __syncthreads();
   tc::fence_after_sync();
   grid_dep_wait();
   grid_dep_launch();
   const uint32_t tmem = S.tmem_base;
+  const auto commit = [](uint64_t* bar) { kPair == 2 ? tc::mma_commit_pair(bar) : tc::mma_commit(bar); };
   const int n_n = (g.N + kBN - 1) / kBN;
-  const int n_units = ((g.M + kF8BM - 1) / kF8BM) * n_n;
+  const int n_units = ((g.M + kPair * kF8BM - 1) / (kPair * kF8BM)) * n_n;
   const int n_k = (g.K + kF8BK - 1) / kF8BK;
 
+  if (warp < 4) tc::reg_dec<kF8RegsLow>();
   if (warp == 0) {
     // ------------------------------------------------------------ TMA loads
     if (lane == 0) {
       uint32_t q = 0;  // K blocks loaded
-      for (int u = blockIdx.x; u < n_units && !*(volatile int*)&S.abort; u += gridDim.x) {
-        const int m0 = (u / n_n) * kF8BM, n0 = (u % n_n) * kBN;
+      for (int u = first_unit; u < n_units && !*(volatile int*)&S.abort; u += unit_step) {
+        const int m0 = (u / n_n * kPair + rank) * kF8BM;
+        const int n0 = (u % n_n) * kBN + (rank * (kBN / kPair));
         for (int kb = 0; kb < n_k; ++kb, ++q) {
           const int s = q % kStages;
           if (!gm_wait(&S.empty[s], ((q / kStages) & 1u) ^ 1u, &S.abort, limit)) break;
-          tc::mbar_expect_tx(&S.full[s], C::kABytes + C::kBBytes);
-          tc::tma_load_2d(tc::smem_u32(stage_a + s * C::kABytes), &map_a, kb * kF8BK, m0, &S.full[s]);
-          tc::tma_load_2d(tc::smem_u32(stage_b + s * C::kBBytes), &map_b, kb * kF8BK, n0, &S.full[s]);
+          const uint32_t sa = tc::smem_u32(stage_a + s * C::kABytes);
+          const uint32_t sb = tc::smem_u32(stage_b + s * C::kBBytes);
+          if (kPair == 2) {
+            // both ranks' loads complete on the even rank's barrier, which
+            // expects them all
+            if (rank == 0) tc::mbar_expect_tx(&S.full[s], 2 * (C::kABytes + C::kBBytes));
+            const uint32_t bar = tc::cluster_map(tc::smem_u32(&S.full[s]), 0);
+            tc::tma_load_2d_pair(sa, &map_a, kb * kF8BK, m0, bar);
+            tc::tma_load_2d_pair(sb, &map_b, kb * kF8BK, n0, bar);
+          } else {
+            tc::mbar_expect_tx(&S.full[s], C::kABytes + C::kBBytes);
+            tc::tma_load_2d(sa, &map_a, kb * kF8BK, m0, &S.full[s]);
+            tc::tma_load_2d(sb, &map_b, kb * kF8BK, n0, &S.full[s]);
+          }
         }
       }
-      // every load issued has landed before the block leaves
-      const uint32_t first = q > (uint32_t)kStages ? q - kStages : 0;
+      // every load issued has landed before the block leaves: the even rank
+      // (which leaves together with the odd one) waits for the last stages.
+      // After an abort it may have fewer to wait for than the odd rank has in
+      // flight, which then gives them time (far more than a load takes).
+      if (kPair == 2 && *(volatile int*)&S.abort) {
+        const long long t0 = clock64();
+        while (clock64() - t0 < 2000000) {
+        }
+      }
+      const uint32_t first = rank ? q : q > (uint32_t)kStages ? q - kStages : 0;
       for (uint32_t p = first; p < q; ++p) {
         const long long t0 = clock64();
         while (!tc::mbar_test(&S.full[p % kStages], (p / kStages) & 1u)) {
@@ -156,94 +230,201 @@ __global__ void __launch_bounds__(kF8Threads, 1)
       }
     }
     __syncwarp();
-  } else if (warp == 1) {
+  } else if (warp <= 2) {
     // ------------------------------------------------------------ MMA issue
-    if (lane == 0) {
-      constexpr uint32_t idesc = tc::idesc_e4m3(kF8BM, kBN);
-      uint32_t q = 0;
-      bool ok = true;
-      for (int u = blockIdx.x; u < n_units && ok; u += gridDim.x) {
-        for (int kb = 0; kb < n_k; ++kb, ++q) {
+    // The whole warp runs the loop, so that its addresses stay uniform; one
+    // lane issues.
+    if (rank == 0) {
+      constexpr uint32_t idesc = tc::idesc_e4m3(kPair * kF8BM, kBN);
+      // all the blocks of this CTA's tiles, one after the other
+      const uint32_t n_q = (n_units - first_unit + unit_step - 1) / unit_step * (uint32_t)n_k;
+      for (uint32_t q = warp - 1; q < n_q; q += 2) {
           const int s = q % kStages, b = q % kBufs;
-          if (!gm_wait(&S.acc_empty[b], ((q / kBufs) & 1u) ^ 1u, &S.abort, limit) ||
-              !gm_wait(&S.full[s], (q / kStages) & 1u, &S.abort, limit)) {
-            ok = false;
-            break;
-          }
-          tc::fence_after_sync();
+          bool ok = f8_wait(&S.full[s], (q / kStages) & 1u, &S.abort, limit);
           const uint64_t da = tc::sdesc_sw128(tc::smem_u32(stage_a + s * C::kABytes), 16, 1024);
+          ok = ok && f8_wait(&S.acc_empty[b], ((q / kBufs) & 1u) ^ 1u, &S.abort, limit);
+          if (!__all_sync(0xffffffffu, ok)) break;
+          tc::fence_after_sync();
           const uint64_t db = tc::sdesc_sw128(tc::smem_u32(stage_b + s * C::kBBytes), 16, 1024);
+          const uint32_t d = tmem + b * kBN;
+          if (tc::elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)  // 32 codes = two 16-byte units along K
-            tc::mma_e4m3(tmem + b * kBN, da + 2 * kk, db + 2 * kk, idesc, kk > 0 ? 1u : 0u);
-          tc::mma_commit(&S.empty[s]);
-          tc::mma_commit(&S.acc_full[b]);
-        }
+            for (int kk = 0; kk < 4; ++kk) {  // 32 codes = two 16-byte units along K
+              if (kPair == 2)
+                tc::mma_e4m3_pair(d, da + 2 * kk, db + 2 * kk, idesc, kk > 0 ? 1u : 0u);
+              else
+                tc::mma_e4m3(d, da + 2 * kk, db + 2 * kk, idesc, kk > 0 ? 1u : 0u);
+            }
+            commit(&S.acc_full[b]);
+            commit(&S.empty[s]);
+          }
+          __syncwarp();
       }
       // every MMA issued has finished before tensor memory is freed
-      tc::mma_commit(&S.mma_done);
-      const long long t0 = clock64();
-      while (!tc::mbar_test(&S.mma_done, 0)) {
-        if (clock64() - t0 > limit) {
-          record_status(tc::kErrTimeout);
-          break;
+      if (tc::elect_one()) {
+        commit(&S.mma_done[warp - 1]);
+        const long long t0 = clock64();
+        while (!tc::mbar_test(&S.mma_done[warp - 1], 0)) {
+          if (clock64() - t0 > limit) {
+            record_status(tc::kErrTimeout);
+            break;
+          }
         }
       }
     }
     __syncwarp();
-  } else {
-    // ------------------------------------------------------------ epilogue
-    const int sub = warp & 3;          // TMEM lanes 32 * sub .. 32 * sub + 31
-    const int half = (warp - 2) >> 2;  // which half of the tile's columns
-    const int et = (sub << 5) | lane;  // row in the tile
-    uint8_t* stg = stage_out + (warp - 2) * (32 * 128);
-    uint8_t* my_row = stg + lane * 128;
-    const uint32_t lane_base = tmem + ((uint32_t)(sub * 32) << 16) + half * kCols;
+  } else if (warp < 4) {
+    // ------------------------------------------------------------ scales
+    // Lane t has rows t, t + 32, .. (and columns t, t + 32, ..); four blocks'
+    // scales are in flight at once.
+    constexpr int kC = kColScale ? kBN / 32 : 2;
     uint32_t q = 0;
     bool ok = true;
-    for (int u = blockIdx.x; u < n_units; u += gridDim.x) {
-      const int m0 = (u / n_n) * kF8BM, c0 = (u % n_n) * kBN + half * kCols;
-      const int row = m0 + et;
-      const float* sa = g.sa + (size_t)(row < g.M ? row : 0) * n_k;
-      // past N every code is zero, and any finite scale will do
-      const int nb = kColScale ? 0 : (c0 < g.N ? c0 : 0) / g.b_rows;
-      const float* sb = g.sb + (size_t)nb * n_k;
+    for (int u = first_unit; u < n_units && ok; u += unit_step) {
+      const int m0 = (u / n_n * kPair + rank) * kF8BM, n0 = (u % n_n) * kBN;
+      // past the ends every code is zero, and any row's scale will do
+      const float* pa[4];
+      const float* pb[kC];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = m0 + lane + 32 * i;
+        pa[i] = g.sa + (size_t)(r < g.M ? r : 0) * n_k;
+      }
+#pragma unroll
+      for (int i = 0; i < kC; ++i) {
+        const int n = kColScale ? n0 + lane + 32 * i : n0 + i * kCols;
+        pb[i] = g.sb + (size_t)(n < g.N ? (kColScale ? n : n / g.b_rows) : 0) * n_k;
+      }
+      for (int kb = 0; kb < n_k && ok; kb += 4, ++q) {
+        float va[4][4], vb[kC][4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int k = kb + j < n_k ? kb + j : n_k - 1;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) va[i][j] = pa[i][k];
+#pragma unroll
+          for (int i = 0; i < kC; ++i) vb[i][j] = pb[i][k];
+        }
+        const int slot = q % kF8Slots;
+        ok = f8_wait(&S.sc_empty[slot], ((q / kF8Slots) & 1u) ^ 1u, &S.abort, limit);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (kColScale) {
+            S.rs[slot][0][lane + 32 * i] = make_float4(va[i][0], va[i][1], va[i][2], va[i][3]);
+          } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              S.rs[slot][h][lane + 32 * i] = make_float4(va[i][0] * vb[h][0], va[i][1] * vb[h][1],
+                                                      va[i][2] * vb[h][2], va[i][3] * vb[h][3]);
+          }
+        }
+        if (kColScale) {
+#pragma unroll
+          for (int i = 0; i < kC; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) S.cs[slot][j][lane + 32 * i] = vb[i][j];
+        }
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&S.sc_full[slot]);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    tc::reg_inc<kF8RegsHigh>();
+    const int sub = warp & 3;          // TMEM lanes 32 * sub .. 32 * sub + 31
+    const int half = (warp - 4) >> 2;  // which half of the tile's columns
+    const int et = (sub << 5) | lane;  // row in the tile
+    uint8_t* stg = stage_out + (warp - 4) * (C::kOutBoxes * 4096);
+    uint8_t* my_row = stg + lane * 128;
+    const int swz = lane & 7;
+    // where this warp's arrivals free a buffer
+    uint32_t free_bar = tc::smem_u32(&S.acc_empty[0]);
+    if (kPair == 2) free_bar = tc::cluster_map(free_bar, 0);
+    const uint32_t lane_base = tmem + ((uint32_t)(sub * 32) << 16) + half * kCols;
+    uint32_t q = 0, qs = 0;
+    bool ok = true;
+    for (int u = first_unit; u < n_units; u += unit_step) {
+      const int m0 = (u / n_n * kPair + rank) * kF8BM, c0 = (u % n_n) * kBN + half * kCols;
       float acc[kCols];
 #pragma unroll
       for (int e = 0; e < kCols; ++e) acc[e] = 0.f;
-      float s_next = sa[0] * (kColScale ? 1.f : sb[0]);
-      for (int kb = 0; kb < n_k; ++kb, ++q) {
-        const int b = q % kBufs;
-        const float s = s_next;
-        if (kb + 1 < n_k) s_next = sa[kb + 1] * (kColScale ? 1.f : sb[kb + 1]);
-        float* cs = S.sb[kb & 1] + half * kCols;
-        if (kColScale) {
-          // this block's column scales: written while the other parity may
-          // still be read; the barrier orders both
-          if (et < kCols) cs[et] = c0 + et < g.N ? g.sb[(size_t)(c0 + et) * n_k + kb] : 0.f;
-          asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
-        }
+      for (int kb4 = 0; kb4 < n_k; kb4 += 4, ++qs) {
+        const int slot = qs % kF8Slots;
         // after an abort every wait returns at once; the loop runs on to its
-        // end (reading stale totals), since the warps share its barriers
-        ok &= gm_wait(&S.acc_full[b], (q / kBufs) & 1u, &S.abort, limit);
-        tc::fence_after_sync();
+        // end (adding stale sums), since the warps share its barriers
+        ok &= f8_wait(&S.sc_full[slot], (qs / kF8Slots) & 1u, &S.abort, limit);
+        const float4 s4 = S.rs[slot][kColScale ? 0 : half][et];
+        const float sj[4] = {s4.x, s4.y, s4.z, s4.w};
 #pragma unroll
-        for (int c = 0; c < kCols / 32; ++c) {
-          float v[32];
-          tc::tmem_ld32(lane_base + b * kBN + 32 * c, v);
-          tc::tmem_ld_wait();
-          tc::tmem_pin<32>(v);
-          if (c == kCols / 32 - 1) {  // the buffer is read: free it
-            tc::fence_before_sync();
-            tc::mbar_arrive(&S.acc_empty[b]);
+        for (int j = 0; j < 4; ++j, ++q) {
+          if (kb4 + j >= n_k) break;
+          const int b = q % kBufs;
+          const float s = sj[j];
+          const float* cs = S.cs[kColScale ? slot : 0][j] + (kColScale ? half * kCols : 0);
+          ok &= f8_wait(&S.acc_full[b], (q / kBufs) & 1u, &S.abort, limit);
+          tc::fence_after_sync();
+          // kChunk columns are added while the next kChunk are read
+          const uint32_t taddr = lane_base + b * kBN;
+          float v[2][kChunk];
+#pragma unroll
+          for (int e = 0; e < kChunk; e += 16) tc::tmem_ld16(taddr + e, v[0] + e);
+#pragma unroll
+          for (int c = 0; c < kCols / kChunk; ++c) {
+            tc::tmem_ld_wait();
+            tc::tmem_pin<kChunk>(v[c & 1]);
+            if (c + 1 < kCols / kChunk) {
+#pragma unroll
+              for (int e = 0; e < kChunk; e += 16)
+                tc::tmem_ld16(taddr + (c + 1) * kChunk + e, v[(c + 1) & 1] + e);
+            } else {  // the buffer is read: free it
+              tc::fence_before_sync();
+              __syncwarp();
+              if (kPair == 2)
+                tc::mbar_arrive_cluster(free_bar + 8 * b, lane == 0);
+              else
+                tc::mbar_arrive_if(free_bar + 8 * b, lane == 0);
+            }
+#pragma unroll
+            for (int e = 0; e < kChunk; e += 4) {
+              float4 k4 = make_float4(s, s, s, s);
+              if (kColScale) {
+                const float4 t = *reinterpret_cast<const float4*>(cs + c * kChunk + e);
+                k4 = make_float4(s * t.x, s * t.y, s * t.z, s * t.w);
+              }
+              float* t = acc + c * kChunk + e;
+              const float* x = v[c & 1] + e;
+              const float2 lo = __ffma2_rn(make_float2(x[0], x[1]), make_float2(k4.x, k4.y),
+                                           make_float2(t[0], t[1]));
+              const float2 hi = __ffma2_rn(make_float2(x[2], x[3]), make_float2(k4.z, k4.w),
+                                           make_float2(t[2], t[3]));
+              t[0] = lo.x; t[1] = lo.y; t[2] = hi.x; t[3] = hi.y;
+            }
           }
-#pragma unroll
-          for (int e = 0; e < 32; ++e)
-            acc[32 * c + e] = fmaf(v[e], kColScale ? s * cs[32 * c + e] : s, acc[32 * c + e]);
         }
+        __syncwarp();
+        tc::mbar_arrive_if(tc::smem_u32(&S.sc_empty[slot]), lane == 0);  // its scales are read
       }
       if (f8_any(!ok)) break;  // all of them, or none
-      const bool live = row < g.M;
+      // The output leaves through the warp's staging rows by TMA, which clips
+      // it to [M, N], while the next tile is under way: wait_staging() waits
+      // for the last tile's, store_boxes() sends this one's.
+      const auto wait_staging = [&] {
+        if (lane == 0) tc::bulk_wait_read();
+        __syncwarp();
+      };
+      const auto store_boxes = [&](int col, int step, int boxes) {
+        tc::fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          for (int i = 0; i < boxes; ++i)
+            if (m0 + sub * 32 < g.M && col + i * step < g.N)
+              tc::tma_store_2d(&map_c, col + i * step, m0 + sub * 32, tc::smem_u32(stg) + i * 4096);
+          tc::bulk_commit();
+        }
+        __syncwarp();
+      };
       if (g.bias) {
 #pragma unroll
         for (int e = 0; e < kCols; e += 8) {
@@ -265,77 +446,55 @@ __global__ void __launch_bounds__(kF8Threads, 1)
 #pragma unroll
         for (int e = 0; e < kCols; ++e) m = max(m, c0 + e < g.N ? mag_bits(acc[e]) : 0u);
         const float am = block_amax(m), inv = kE4m3Max / am;
-        if (live && c0 < g.N)
-          a.qs[(size_t)row * ((g.N + 127) >> 7) + (c0 >> 7)] = am / kE4m3Max;
+        if (m0 + et < g.M && c0 < g.N)
+          a.qs[(size_t)(m0 + et) * ((g.N + 127) >> 7) + (c0 >> 7)] = am / kE4m3Max;
+        wait_staging();
 #pragma unroll
         for (int p = 0; p < kCols / 16; ++p) {
           const float* v = acc + 16 * p;
-          *reinterpret_cast<uint4*>(my_row + ((p ^ (lane & 7)) << 4)) = make_uint4(
+          *reinterpret_cast<uint4*>(my_row + ((p ^ swz) << 4)) = make_uint4(
               e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
               e4m3x4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv),
               e4m3x4(v[8] * inv, v[9] * inv, v[10] * inv, v[11] * inv),
               e4m3x4(v[12] * inv, v[13] * inv, v[14] * inv, v[15] * inv));
         }
-        __syncwarp();
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int rl = 4 * k + (lane >> 3), p = lane & 7;
-          const int r = m0 + sub * 32 + rl, col = c0 + 16 * p;
-          const uint4 w = *reinterpret_cast<const uint4*>(stg + rl * 128 + ((p ^ (rl & 7)) << 4));
-          if (r < g.M && col < g.N) *reinterpret_cast<uint4*>(a.Q + (size_t)r * g.N + col) = w;
-        }
-        __syncwarp();
+        store_boxes(c0, 128, 1);
       } else if (!g.c_f32) {
-        // 64 columns of bf16 fill a staging row; eight lanes write it out
+        wait_staging();
 #pragma unroll
-        for (int h = 0; h < kCols / 64; ++h) {
-#pragma unroll
-          for (int p = 0; p < 8; ++p) {
-            const float* v = acc + 64 * h + 8 * p;
-            *reinterpret_cast<uint4*>(my_row + ((p ^ (lane & 7)) << 4)) =
-                make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                           pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-          }
-          __syncwarp();
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int rl = 4 * k + (lane >> 3), p = lane & 7;
-            const int r = m0 + sub * 32 + rl, col = c0 + 64 * h + 8 * p;
-            const uint4 w = *reinterpret_cast<const uint4*>(stg + rl * 128 + ((p ^ (rl & 7)) << 4));
-            if (r < g.M && col < g.N)
-              *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(g.C) + (size_t)r * g.N + col) = w;
-          }
-          __syncwarp();
+        for (int p = 0; p < kCols / 8; ++p) {
+          const float* v = acc + 8 * p;
+          *reinterpret_cast<uint4*>(my_row + (p >> 3) * 4096 + (((p & 7) ^ swz) << 4)) =
+              make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                         pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
         }
+        store_boxes(c0, 64, kCols / 64);
       } else {
 #pragma unroll
-        for (int h = 0; h < kCols / 32; ++h) {
+        for (int h = 0; h < 2; ++h) {
+          wait_staging();
 #pragma unroll
-          for (int p = 0; p < 8; ++p) {
-            const float* v = acc + 32 * h + 4 * p;
-            *reinterpret_cast<float4*>(my_row + ((p ^ (lane & 7)) << 4)) =
+          for (int p = 0; p < kCols / 8; ++p) {
+            const float* v = acc + h * (kCols / 2) + 4 * p;
+            *reinterpret_cast<float4*>(my_row + (p >> 3) * 4096 + (((p & 7) ^ swz) << 4)) =
                 make_float4(v[0], v[1], v[2], v[3]);
           }
-          __syncwarp();
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int rl = 4 * k + (lane >> 3), p = lane & 7;
-            const int r = m0 + sub * 32 + rl, col = c0 + 32 * h + 4 * p;
-            const float4 w =
-                *reinterpret_cast<const float4*>(stg + rl * 128 + ((p ^ (rl & 7)) << 4));
-            if (r < g.M && col < g.N)
-              *reinterpret_cast<float4*>(static_cast<float*>(g.C) + (size_t)r * g.N + col) = w;
-          }
-          __syncwarp();
+          store_boxes(c0 + h * (kCols / 2), 32, kCols / 64);
         }
       }
     }
+    if (lane == 0) tc::bulk_wait();
+    __syncwarp();
   }
   tc::fence_before_sync();
   __syncthreads();
+  if (kPair == 2) tc::cluster_sync();  // neither leaves while the other may still reach it
   if (warp == 1) {
     tc::fence_after_sync();
-    tc::tmem_dealloc(tmem, 512);
+    if (kPair == 2)
+      tc::tmem_dealloc_pair(tmem, 512);
+    else
+      tc::tmem_dealloc(tmem, 512);
   }
 }
 
