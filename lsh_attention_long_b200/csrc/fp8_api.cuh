@@ -130,7 +130,7 @@ bool u8_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint
   return map_128b(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, base, rows, cols, box_rows);
 }
 
-template <int kPair, int kBN, int kEpi, bool kColScale>
+template <int kPair, int kBN, int kEpi, bool kColScale, int kParts>
 lsh_status fp8_tc_launch(const lsh::Fp8TcArgs& a, cudaStream_t st) {
   const lsh::Fp8GemmArgs& g = a.g;
   CUtensorMap ma, mb, mc;
@@ -143,7 +143,7 @@ lsh_status fp8_tc_launch(const lsh::Fp8TcArgs& a, cudaStream_t st) {
                   : map_128b(&mc, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, g.C, M, N, 32)))
     return LSH_ERR_CUDA;
   constexpr size_t smem = lsh::fp8_tc_smem_bytes<kPair, kBN, kEpi, kColScale>();
-  const auto kernel = lsh::gemm_fp8_tc_kernel<kPair, kBN, kEpi, kColScale>;
+  const auto kernel = lsh::gemm_fp8_tc_kernel<kPair, kBN, kEpi, kColScale, kParts>;
   // the kernel's register split adds up only if it was built with kF8Regs
   static const bool regs_ok = [&] {
     cudaFuncAttributes at;
@@ -155,35 +155,84 @@ lsh_status fp8_tc_launch(const lsh::Fp8TcArgs& a, cudaStream_t st) {
   const long long units = (long long)ceil_div(g.M, kPair * lsh::kF8BM) * ceil_div(g.N, kBN);
   if (units > 0x3fffffff) return LSH_ERR_UNSUPPORTED;
   const int fit = num_sms() / kPair;
-  return launch_pdl_cluster(kernel, dim3((unsigned)((units < fit ? units : fit) * kPair)),
-                    dim3(lsh::kF8Threads), smem, st, kPair, ma, mb, mc, a);
+  const int clusters = kParts > 1 || units < fit ? (int)units : fit;
+  return launch_pdl_cluster(kernel, dim3((unsigned)(clusters * kPair * kParts)),
+                            dim3(lsh::kF8Threads), smem, st, kPair * kParts, ma, mb, mc, a);
 }
 
-// Tiles: a pair of CTAs on 256 x 256 once those alone give every other SM one
-// (a lone tile of 128 x 128 needs twice the loads per product), else 128 x 128.
-lsh_status fp8_gemm_launch(const lsh::Fp8GemmArgs& g, cudaStream_t st) {
+template <int kNT, int kRG, int kW, int kEpi>
+lsh_status fp8_skinny_launch(const lsh::Fp8SkinnyArgs& a, cudaStream_t st) {
+  // a cluster covers 128 rows of B, one block of the 8-bit result
+  constexpr int kRows = 16 * kRG, kCluster = kEpi == lsh::kF8Quant ? 128 / kRows : 1;
+  const int grid = ceil_div(ceil_div(a.g.N, kRows), kCluster) * kCluster;
+  return launch_pdl_cluster(lsh::gemm_fp8_skinny_kernel<kNT, kRG, kW, kEpi>, dim3((unsigned)grid),
+                            dim3(32 * kW), 0, st, kCluster, a);
+}
+// Blocks of 4 warps where there are two or more for every SM, else of 8, which
+// read a row group in half the time.
+template <int kEpi>
+lsh_status fp8_skinny_launch(const lsh::Fp8GemmArgs& g, void* Q, float* qs, int early_b,
+                             cudaStream_t st) {
+  lsh::Fp8SkinnyArgs a = {};
+  a.g = g;
+  a.Q = static_cast<uint8_t*>(Q);
+  a.qs = qs;
+  a.early_b = early_b;
+  const int rows = g.M <= 8 ? 16 : 32;
+  const bool many = ceil_div(g.N, rows) >= 2 * num_sms();
+  if (g.M <= 8)
+    return many ? fp8_skinny_launch<1, 1, 4, kEpi>(a, st) : fp8_skinny_launch<1, 1, 8, kEpi>(a, st);
+  return many ? fp8_skinny_launch<2, 2, 4, kEpi>(a, st) : fp8_skinny_launch<2, 2, 8, kEpi>(a, st);
+}
+
+// Whether 256 x 256 tiles, on a pair of CTAs each, are enough to occupy half of
+// the SMs: they need half the loads per product of 128 x 128 tiles.
+bool fp8_pair_tiles(const lsh::Fp8GemmArgs& g) {
+  return 4LL * ceil_div(g.M, 256) * ceil_div(g.N, 256) >= num_sms();
+}
+
+// CTAs that share a 128 x 128 tile's K: as many (up to 8) as leave each two
+// blocks of K and all of them an SM at the same time (clusters of 4 and 8 fit
+// on 132 and 120 SMs).
+int fp8_split(const lsh::Fp8GemmArgs& g) {
+  const long long tiles = (long long)ceil_div(g.M, 128) * ceil_div(g.N, 128);
+  const int k = ceil_div(g.K, 128);
+  if (tiles * 8 <= 120 && k >= 16) return 8;
+  if (tiles * 4 <= 132 && k >= 8) return 4;
+  if (tiles * 2 <= num_sms() && k >= 4) return 2;
+  return 1;
+}
+
+template <bool kColScale>
+lsh_status fp8_tc_gemm(const lsh::Fp8TcArgs& a, cudaStream_t st) {
+  if (fp8_pair_tiles(a.g)) return fp8_tc_launch<2, 256, lsh::kF8Store, kColScale, 1>(a, st);
+  const int parts = fp8_split(a.g);
+  if (parts == 8) return fp8_tc_launch<1, 128, lsh::kF8Store, kColScale, 8>(a, st);
+  if (parts == 4) return fp8_tc_launch<1, 128, lsh::kF8Store, kColScale, 4>(a, st);
+  if (parts == 2) return fp8_tc_launch<1, 128, lsh::kF8Store, kColScale, 2>(a, st);
+  return fp8_tc_launch<1, 128, lsh::kF8Store, kColScale, 1>(a, st);
+}
+
+// early_b: see Fp8SkinnyArgs.
+lsh_status fp8_gemm_launch(const lsh::Fp8GemmArgs& g, cudaStream_t st, int early_b = 0) {
+  if (g.M <= lsh::kSkMaxM)
+    return fp8_skinny_launch<lsh::kF8Store>(g, nullptr, nullptr, early_b, st);
   lsh::Fp8TcArgs a = {};
   a.g = g;
   a.wait_limit = g_wait_limit;
-  const long long units = (long long)ceil_div(g.M, 256) * ceil_div(g.N, 256);
-  const bool pair = units * 4 >= num_sms();
-  if (g.b_rows == 1)
-    return pair ? fp8_tc_launch<2, 256, lsh::kF8Store, true>(a, st)
-                : fp8_tc_launch<1, 128, lsh::kF8Store, true>(a, st);
-  return pair ? fp8_tc_launch<2, 256, lsh::kF8Store, false>(a, st)
-              : fp8_tc_launch<1, 128, lsh::kF8Store, false>(a, st);
+  return g.b_rows == 1 ? fp8_tc_gemm<true>(a, st) : fp8_tc_gemm<false>(a, st);
 }
 
 // The hidden activation of the feed-forward: max(0, A B^T + bias) in 8 bits.
 lsh_status fp8_gemm_quant_launch(const lsh::Fp8GemmArgs& g, void* Q, float* qs, cudaStream_t st) {
+  if (g.M <= lsh::kSkMaxM) return fp8_skinny_launch<lsh::kF8Quant>(g, Q, qs, 0, st);
   lsh::Fp8TcArgs a = {};
   a.g = g;
   a.Q = static_cast<uint8_t*>(Q);
   a.qs = qs;
   a.wait_limit = g_wait_limit;
-  const long long units = (long long)ceil_div(g.M, 256) * ceil_div(g.N, 256);
-  return units * 4 >= num_sms() ? fp8_tc_launch<2, 256, lsh::kF8Quant, false>(a, st)
-                                : fp8_tc_launch<1, 256, lsh::kF8Quant, false>(a, st);
+  return fp8_pair_tiles(g) ? fp8_tc_launch<2, 256, lsh::kF8Quant, false, 1>(a, st)
+                           : fp8_tc_launch<1, 128, lsh::kF8Quant, false, 1>(a, st);
 }
 
 lsh::Fp8GemmArgs fp8_gemm_args(int M, int N, int K, const void* A, const float* sa, const void* B,
@@ -420,7 +469,9 @@ lsh_status lsh_ffn_forward_fp8(int32_t tokens, int32_t d_model, int32_t d_ff, in
     lsh::Fp8GemmArgs g2 = fp8_gemm_args(n, d_model, d_ff, w + l.h8, hs, W2, w2_scales, 128);
     g2.bias = static_cast<const __nv_bfloat16*>(b2);
     g2.C = static_cast<__nv_bfloat16*>(Y) + c0 * d_model;
-    if ((s = fp8_gemm_launch(g2, st)) != LSH_OK) return s;
+    // W2: complete before the hidden product's wait returned, which was
+    // before this launch could start
+    if ((s = fp8_gemm_launch(g2, st, 1)) != LSH_OK) return s;
   }
   return LSH_OK;
 }

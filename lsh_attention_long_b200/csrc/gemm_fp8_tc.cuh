@@ -12,7 +12,9 @@
 // kPair 2: two CTAs (a cluster) work on a 256 x 256 tile with pair MMAs.  Each
 // loads its own 128 rows of A and half of B's, 32 KB per block of K in place
 // of the 48 KB of a 128 x 256 tile alone, which the path from L2 would bound.
-// kPair 1 serves products with few tiles.
+// kPair 1 (tiles of 128 x 128) serves products with few tiles; with kParts the
+// CTAs of a cluster share out a tile's K and add their totals up through
+// distributed shared memory.
 //
 // Warp roles (384 threads, persistent blocks, one per SM):
 //   warp 0      one thread loads A and B tiles of 128-byte rows with TMA
@@ -82,6 +84,7 @@ struct Fp8Smem {
   uint64_t acc_full[C::kBufs], acc_empty[C::kBufs];
   uint64_t sc_full[kF8Slots], sc_empty[kF8Slots];
   uint64_t mma_done[2];
+  uint32_t amax[2][kEpi == kF8Quant && kBN == 128 ? kF8BM : 1];
   uint32_t tmem_base;
   int abort;
 };
@@ -118,14 +121,15 @@ __device__ __forceinline__ bool f8_any(bool pred) {
   return r != 0;
 }
 
-template <int kPair, int kBN, int kEpi, bool kColScale>
+template <int kPair, int kBN, int kEpi, bool kColScale, int kParts>
 __global__ void __launch_bounds__(kF8Threads, 1)
     gemm_fp8_tc_kernel(const __grid_constant__ CUtensorMap map_a,
                        const __grid_constant__ CUtensorMap map_b,
                        const __grid_constant__ CUtensorMap map_c, Fp8TcArgs a) {
   using C = Fp8Cfg<kPair, kBN, kEpi, kColScale>;
   using Smem = Fp8Smem<kPair, kBN, kEpi, kColScale>;
-  static_assert(kEpi != kF8Quant || kBN == 256, "a thread's columns are one block");
+  constexpr bool kSplit = kParts > 1;
+  static_assert(!kSplit || (kPair == 1 && kBN == 128 && kEpi == kF8Store), "split of K");
   constexpr int kStages = C::kStages, kBufs = C::kBufs;
   constexpr int kCols = C::kCols;
   extern __shared__ uint8_t smem_raw[];
@@ -139,7 +143,9 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const long long limit = a.wait_limit;
   const int rank = kPair == 2 ? (int)tc::cluster_rank() : 0;
-  const int first_unit = blockIdx.x / kPair, unit_step = gridDim.x / kPair;
+  // kSplit: a cluster shares one tile's blocks of K
+  const int part = kSplit ? (int)tc::cluster_rank() : 0;
+  const int first_unit = blockIdx.x / (kPair * kParts), unit_step = gridDim.x / (kPair * kParts);
 
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -180,7 +186,9 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   const auto commit = [](uint64_t* bar) { kPair == 2 ? tc::mma_commit_pair(bar) : tc::mma_commit(bar); };
   const int n_n = (g.N + kBN - 1) / kBN;
   const int n_units = ((g.M + kPair * kF8BM - 1) / (kPair * kF8BM)) * n_n;
-  const int n_k = (g.K + kF8BK - 1) / kF8BK;
+  const int k_all = (g.K + kF8BK - 1) / kF8BK;  // blocks of K: all, and this CTA's
+  const int k_lo = kSplit ? part * k_all / kParts : 0;
+  const int n_k = kSplit ? (part + 1) * k_all / kParts - k_lo : k_all;
 
   if (warp < 4) tc::reg_dec<kF8RegsLow>();
   if (warp == 0) {
@@ -200,12 +208,12 @@ __global__ void __launch_bounds__(kF8Threads, 1)
             // expects them all
             if (rank == 0) tc::mbar_expect_tx(&S.full[s], 2 * (C::kABytes + C::kBBytes));
             const uint32_t bar = tc::cluster_map(tc::smem_u32(&S.full[s]), 0);
-            tc::tma_load_2d_pair(sa, &map_a, kb * kF8BK, m0, bar);
-            tc::tma_load_2d_pair(sb, &map_b, kb * kF8BK, n0, bar);
+            tc::tma_load_2d_pair(sa, &map_a, (k_lo + kb) * kF8BK, m0, bar);
+            tc::tma_load_2d_pair(sb, &map_b, (k_lo + kb) * kF8BK, n0, bar);
           } else {
             tc::mbar_expect_tx(&S.full[s], C::kABytes + C::kBBytes);
-            tc::tma_load_2d(sa, &map_a, kb * kF8BK, m0, &S.full[s]);
-            tc::tma_load_2d(sb, &map_b, kb * kF8BK, n0, &S.full[s]);
+            tc::tma_load_2d(sa, &map_a, (k_lo + kb) * kF8BK, m0, &S.full[s]);
+            tc::tma_load_2d(sb, &map_b, (k_lo + kb) * kF8BK, n0, &S.full[s]);
           }
         }
       }
@@ -288,12 +296,12 @@ __global__ void __launch_bounds__(kF8Threads, 1)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int r = m0 + lane + 32 * i;
-        pa[i] = g.sa + (size_t)(r < g.M ? r : 0) * n_k;
+        pa[i] = g.sa + (size_t)(r < g.M ? r : 0) * k_all + k_lo;
       }
 #pragma unroll
       for (int i = 0; i < kC; ++i) {
         const int n = kColScale ? n0 + lane + 32 * i : n0 + i * kCols;
-        pb[i] = g.sb + (size_t)(n < g.N ? (kColScale ? n : n / g.b_rows) : 0) * n_k;
+        pb[i] = g.sb + (size_t)(n < g.N ? (kColScale ? n : n / g.b_rows) : 0) * k_all + k_lo;
       }
       for (int kb = 0; kb < n_k && ok; kb += 4, ++q) {
         float va[4][4], vb[kC][4];
@@ -406,7 +414,56 @@ __global__ void __launch_bounds__(kF8Threads, 1)
         __syncwarp();
         tc::mbar_arrive_if(tc::smem_u32(&S.sc_empty[slot]), lane == 0);  // its scales are read
       }
-      if (f8_any(!ok)) break;  // all of them, or none
+      const bool bad = f8_any(!ok);  // for all of them, or none
+      if (bad && !kSplit) break;
+      if (kSplit) {
+        // Each CTA of the cluster adds up kCols / kParts columns of every
+        // thread's totals, in the order of the parts; they travel through the
+        // stages, which all of the tile's MMAs have left.
+        constexpr int kW = kCols / kParts, kW4 = kW / 4;
+        float4* const inbox = reinterpret_cast<float4*>(sm) + (tid - 128);  // [from][kW4][256]
+        tc::cluster_sync();  // every CTA's MMAs are done (warps 0-3 take part below)
+        if (!bad) {
+#pragma unroll
+          for (int to = 0; to < kParts; ++to) {
+            const uint32_t at = tc::cluster_map(tc::smem_u32(inbox + part * (kW4 * 256)), to);
+#pragma unroll
+            for (int j = 0; j < kW4; ++j) tc::st_cluster(at + j * 4096, acc + to * kW + 4 * j);
+          }
+        }
+        tc::cluster_sync();
+        const int row = m0 + et, col = c0 + part * kW;
+        if (!bad && row < g.M) {
+#pragma unroll
+          for (int j = 0; j < kW4; ++j) {
+            const int c = col + 4 * j;
+            if (c >= g.N) break;
+            float o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int from = 0; from < kParts; ++from) {
+              const float4 x = inbox[(from * kW4 + j) * 256];
+              o[0] += x.x; o[1] += x.y; o[2] += x.z; o[3] += x.w;
+            }
+            if (g.bias) {
+              const uint2 bv = *reinterpret_cast<const uint2*>(g.bias + c);
+              const float2 lo = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&bv.x));
+              const float2 hi = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&bv.y));
+              o[0] += lo.x; o[1] += lo.y; o[2] += hi.x; o[3] += hi.y;
+            }
+            if (g.relu) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) o[i] = o[i] < 0.f ? 0.f : o[i];  // a NaN stays one
+            }
+            if (g.c_f32)
+              *reinterpret_cast<float4*>(static_cast<float*>(g.C) + (size_t)row * g.N + c) =
+                  make_float4(o[0], o[1], o[2], o[3]);
+            else
+              *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(g.C) + (size_t)row * g.N + c) =
+                  make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
+          }
+        }
+        break;  // a cluster has one tile
+      }
       // The output leaves through the warp's staging rows by TMA, which clips
       // it to [M, N], while the next tile is under way: wait_staging() waits
       // for the last tile's, store_boxes() sends this one's.
@@ -441,24 +498,35 @@ __global__ void __launch_bounds__(kF8Threads, 1)
         for (int e = 0; e < kCols; ++e) acc[e] = acc[e] < 0.f ? 0.f : acc[e];  // a NaN stays one
       }
       if (kEpi == kF8Quant) {
-        // the thread's 128 columns are one block of its row (kBN = 256)
+        // a block is the thread's 128 columns, or (kBN = 128) its 64 and those
+        // of the other warpgroup's thread of the same row
         uint32_t m = 0;
 #pragma unroll
         for (int e = 0; e < kCols; ++e) m = max(m, c0 + e < g.N ? mag_bits(acc[e]) : 0u);
+        if (kCols == 64) {
+          S.amax[half][et] = m;
+          asm volatile("bar.sync 1, 256;" ::: "memory");
+          m = max(m, S.amax[half ^ 1][et]);
+          asm volatile("bar.sync 1, 256;" ::: "memory");
+        }
         const float am = block_amax(m), inv = kE4m3Max / am;
-        if (m0 + et < g.M && c0 < g.N)
+        if (m0 + et < g.M && c0 < g.N && (c0 & 127) == 0)
           a.qs[(size_t)(m0 + et) * ((g.N + 127) >> 7) + (c0 >> 7)] = am / kE4m3Max;
-        wait_staging();
+        if (kCols == 128) wait_staging();
 #pragma unroll
         for (int p = 0; p < kCols / 16; ++p) {
           const float* v = acc + 16 * p;
-          *reinterpret_cast<uint4*>(my_row + ((p ^ swz) << 4)) = make_uint4(
+          const uint4 w = make_uint4(
               e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
               e4m3x4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv),
               e4m3x4(v[8] * inv, v[9] * inv, v[10] * inv, v[11] * inv),
               e4m3x4(v[12] * inv, v[13] * inv, v[14] * inv, v[15] * inv));
+          if (kCols == 128)
+            *reinterpret_cast<uint4*>(my_row + ((p ^ swz) << 4)) = w;
+          else if (m0 + et < g.M && c0 + 16 * p < g.N)  // two whole sectors of the row
+            *reinterpret_cast<uint4*>(a.Q + (size_t)(m0 + et) * g.N + c0 + 16 * p) = w;
         }
-        store_boxes(c0, 128, 1);
+        if (kCols == 128) store_boxes(c0, 128, 1);
       } else if (!g.c_f32) {
         wait_staging();
 #pragma unroll
@@ -485,6 +553,11 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     }
     if (lane == 0) tc::bulk_wait();
     __syncwarp();
+  }
+  if (kSplit && warp < 4) {  // the epilogue's two
+    __syncwarp();
+    tc::cluster_sync();
+    tc::cluster_sync();
   }
   tc::fence_before_sync();
   __syncthreads();

@@ -15,6 +15,7 @@
 #include "common.cuh"
 #include "ffn_tc.cuh"
 #include "gemm_fp8.cuh"
+#include "gemm_fp8_skinny.cuh"
 #include "gemm_fp8_tc.cuh"
 #include "hash_simt.cuh"
 #include "hash_tc.cuh"

@@ -31,21 +31,26 @@ def _up(n: int, to: int) -> int:
     return -(-n // to) * to
 
 
-def _check(specs) -> torch.device:
-    """The device of (name, tensor, shape, dtype) entries, None tensors
+def _check(*specs) -> int:
+    """The device index of (name, tensor, shape, dtype) entries, None tensors
     skipped.  What is wrong is reported by the library's common check, after
     the entries have been gone through once."""
-    dev = None
-    for name, t, shape, dtype in specs:
+    index = None
+    for _, t, shape, dtype in specs:
         if t is None:
             continue
-        if (not isinstance(t, torch.Tensor) or t.shape != shape or t.dtype is not dtype
-                or not t.is_contiguous() or not t.is_cuda
-                or (dev is not None and t.device != dev)):
-            _validate([(n, x, s, d, True) for n, x, s, d in specs])
-        if dev is None:
-            dev = t.device
-    return dev
+        if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape
+                or not t.is_contiguous()):
+            break
+        at = t.get_device()  # -1 on the host
+        if at != index:
+            if index is not None or at < 0:
+                break
+            index = at
+    else:
+        return index
+    _validate([(n, x, s, d, True) for n, x, s, d in specs])
+    raise ValueError("tensors must be on one CUDA device")
 
 
 def _matrix(name: str, t, dtypes) -> Tuple[int, int]:
@@ -57,19 +62,19 @@ def _matrix(name: str, t, dtypes) -> Tuple[int, int]:
     return t.shape
 
 
-def _on(dev: torch.device, stream):
+def _on(index: int, stream):
     """The context in which a call allocates and runs: the tensors' device and
     the stream asked for."""
     if stream is not None:
-        if stream.device != dev:
-            raise ValueError(f"stream is on {stream.device}, expected {dev}")
+        if stream.device.index != index:
+            raise ValueError(f"stream is on {stream.device}, expected cuda:{index}")
         return torch.cuda.stream(stream)
-    return _HERE if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+    return _HERE if index == torch._C._cuda_getDevice() else torch.cuda.device(index)
 
 
-def _go(name: str, *args) -> None:
+def _go(name: str, index: int, *args) -> None:
     rc = getattr(_lsh._lib or load_library(), name)(
-        *args, torch.cuda.current_stream().cuda_stream)
+        *args, torch._C._cuda_getCurrentRawStream(index))
     if rc != 0:
         raise LshError(name, rc)
 
@@ -78,15 +83,15 @@ def _p(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
-def _scratch(name: str, sizes, ws, dev):
+def _scratch(name: str, sizes, ws, index: int):
     """(workspace, pointer, bytes): the caller's, or one of the size the library asks for."""
     if ws is None:
         n = getattr(_lsh._lib or load_library(), name)(*sizes)
         if n == 0:
             return None, None, 0
-        ws = torch.empty(n, dtype=torch.uint8, device=dev)
-    elif not isinstance(ws, torch.Tensor) or ws.device != dev or not ws.is_contiguous():
-        raise ValueError(f"ws must be a contiguous tensor on {dev}")
+        ws = torch.empty(n, dtype=torch.uint8, device=index)
+    elif not isinstance(ws, torch.Tensor) or ws.get_device() != index or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous tensor on cuda:{index}")
     return ws, ws.data_ptr(), ws.numel() * ws.element_size()
 
 
@@ -113,10 +118,10 @@ def lsh_rmsnorm_forward(X, w, *, R=None, eps: float = 1e-6, out_dtype=None, H=No
     f32 = torch.float32
     if yt is not F8:
         scales = None
-    dev = _check((("X", X, shape, X.dtype), ("w", w, (cols,), w.dtype), ("R", R, shape, rt),
+    dev = _check(("X", X, shape, X.dtype), ("w", w, (cols,), w.dtype), ("R", R, shape, rt),
                   ("H", H, shape, X.dtype), ("Y", Y, shape, yt),
                   ("scales", scales, (rows, _up(cols, 128) // 128), f32),
-                  ("rstd", rstd, (rows,), f32)))
+                  ("rstd", rstd, (rows,), f32))
     with _on(dev, stream):
         if R is not None and H is None:
             H = torch.empty_like(X)
@@ -126,7 +131,7 @@ def lsh_rmsnorm_forward(X, w, *, R=None, eps: float = 1e-6, out_dtype=None, H=No
             scales = torch.empty((rows, _up(cols, 128) // 128), dtype=f32, device=dev)
         if rstd is None and want_rstd:
             rstd = torch.empty((rows,), dtype=f32, device=dev)
-        _go("lsh_rmsnorm_forward", rows, cols, _CODES[X.dtype], _CODES[rt], _CODES[w.dtype],
+        _go("lsh_rmsnorm_forward", dev, rows, cols, _CODES[X.dtype], _CODES[rt], _CODES[w.dtype],
             _CODES[yt], X.data_ptr(), _p(R), w.data_ptr(), eps, _p(H), Y.data_ptr(), _p(scales),
             _p(rstd))
     return X if R is None else H, Y, scales, rstd
@@ -142,17 +147,17 @@ def lsh_rmsnorm_backward(dY, H, w, rstd, *, dH=None, dX=None, dw=None, ws=None, 
             raise ValueError(f"{name} must be a tensor of float32 or bfloat16")
     shape, cols, f32 = H.shape, H.shape[-1], torch.float32
     rows = H.numel() // cols if cols else 0
-    dev = _check((("dY", dY, shape, dY.dtype), ("H", H, shape, H.dtype),
+    dev = _check(("dY", dY, shape, dY.dtype), ("H", H, shape, H.dtype),
                   ("w", w, (cols,), w.dtype), ("rstd", rstd, (rows,), f32),
                   ("dH", dH, shape, H.dtype), ("dX", dX, shape, H.dtype),
-                  ("dw", dw, (cols,), f32)))
+                  ("dw", dw, (cols,), f32))
     with _on(dev, stream):
         if dX is None:
             dX = torch.empty_like(H)
         if dw is None:
             dw = torch.empty((cols,), dtype=f32, device=dev)
         ws, wp, wn = _scratch("lsh_rmsnorm_bwd_ws_size", (rows, cols), ws, dev)
-        _go("lsh_rmsnorm_backward", rows, cols, _CODES[H.dtype], _CODES[dY.dtype],
+        _go("lsh_rmsnorm_backward", dev, rows, cols, _CODES[H.dtype], _CODES[dY.dtype],
             _CODES[w.dtype], dY.data_ptr(), H.data_ptr(), w.data_ptr(), rstd.data_ptr(), _p(dH),
             dX.data_ptr(), dw.data_ptr(), wp, wn)
     return dX, dw
@@ -172,9 +177,9 @@ def lsh_quantize_fp8(X, *, block_rows: int = 1, transposed: bool = False, Y=None
     yt_shape = (cols, _up(rows, 16))
     if not transposed and (Yt is not None or scales_t is not None):
         raise ValueError("Yt and scales_t are written only with transposed=True")
-    dev = _check((("X", X, (rows, cols), X.dtype), ("Y", Y, (rows, cols), F8),
+    dev = _check(("X", X, (rows, cols), X.dtype), ("Y", Y, (rows, cols), F8),
                   ("scales", scales, s_shape, f32), ("Yt", Yt, yt_shape, F8),
-                  ("scales_t", scales_t, t_shape, f32)))
+                  ("scales_t", scales_t, t_shape, f32))
     with _on(dev, stream):
         if Y is None:
             Y = torch.empty((rows, cols), dtype=F8, device=dev)
@@ -185,7 +190,7 @@ def lsh_quantize_fp8(X, *, block_rows: int = 1, transposed: bool = False, Y=None
                 Yt = torch.empty(yt_shape, dtype=F8, device=dev)
             if scales_t is None:
                 scales_t = torch.empty(t_shape, dtype=f32, device=dev)
-        _go("lsh_quantize_fp8", rows, cols, _CODES[X.dtype], br, X.data_ptr(), Y.data_ptr(),
+        _go("lsh_quantize_fp8", dev, rows, cols, _CODES[X.dtype], br, X.data_ptr(), Y.data_ptr(),
             scales.data_ptr(), _p(Yt), _p(scales_t))
     return (Y, scales, Yt, scales_t) if transposed else (Y, scales)
 
@@ -201,15 +206,15 @@ def lsh_matmul_fp8(A, a_scales, B, b_scales, *, bias=None, relu: bool = False,
     kb, f32 = _up(K, 128) // 128, torch.float32
     square = (_up(N, 128) // 128, kb)
     rowwise = isinstance(b_scales, torch.Tensor) and N >= 16 and b_scales.shape == (N, kb)
-    dev = _check((("A", A, (M, K), F8), ("a_scales", a_scales, (M, kb), f32),
+    dev = _check(("A", A, (M, K), F8), ("a_scales", a_scales, (M, kb), f32),
                   ("B", B, (N, K), F8),
                   ("b_scales", b_scales, (N, kb) if rowwise else square, f32),
-                  ("bias", bias, (N,), torch.bfloat16), ("C", C, (M, N), out_dtype)))
+                  ("bias", bias, (N,), torch.bfloat16), ("C", C, (M, N), out_dtype))
     with _on(dev, stream):
         if C is None:
             C = torch.empty((M, N), dtype=out_dtype, device=dev)
         ws, wp, wn = _scratch("lsh_matmul_fp8_ws_size", (M, N, K), ws, dev)
-        _go("lsh_matmul_fp8", M, N, K, A.data_ptr(), a_scales.data_ptr(), B.data_ptr(),
+        _go("lsh_matmul_fp8", dev, M, N, K, A.data_ptr(), a_scales.data_ptr(), B.data_ptr(),
             b_scales.data_ptr(), 1 if rowwise else 128, _p(bias), int(relu), _CODES[out_dtype],
             C.data_ptr(), wp, wn)
     return C
@@ -225,9 +230,9 @@ def lsh_matmul_fp8_backward(dC, A, Bt, bt_scales, *, out_dtype=torch.bfloat16, d
     K = _matrix("A", A, (bf,))[1]
     if out_dtype not in _FLOATS:
         raise ValueError(f"out_dtype {out_dtype} is not float32 or bfloat16")
-    dev = _check((("dC", dC, (M, N), bf), ("A", A, (M, K), bf), ("Bt", Bt, (K, N), F8),
+    dev = _check(("dC", dC, (M, N), bf), ("A", A, (M, K), bf), ("Bt", Bt, (K, N), F8),
                   ("bt_scales", bt_scales, (_up(K, 128) // 128, _up(N, 128) // 128), f32),
-                  ("dA", dA, (M, K), out_dtype), ("dB", dB, (N, K), f32), ("db", db, (N,), f32)))
+                  ("dA", dA, (M, K), out_dtype), ("dB", dB, (N, K), f32), ("db", db, (N,), f32))
     with _on(dev, stream):
         if dA is None:
             dA = torch.empty((M, K), dtype=out_dtype, device=dev)
@@ -236,7 +241,7 @@ def lsh_matmul_fp8_backward(dC, A, Bt, bt_scales, *, out_dtype=torch.bfloat16, d
         if db is None:
             db = torch.empty((N,), dtype=f32, device=dev)
         ws, wp, wn = _scratch("lsh_matmul_fp8_bwd_ws_size", (M, N, K), ws, dev)
-        _go("lsh_matmul_fp8_backward", M, N, K, dC.data_ptr(), A.data_ptr(), Bt.data_ptr(),
+        _go("lsh_matmul_fp8_backward", dev, M, N, K, dC.data_ptr(), A.data_ptr(), Bt.data_ptr(),
             bt_scales.data_ptr(), _CODES[out_dtype], dA.data_ptr(), dB.data_ptr(), db.data_ptr(),
             wp, wn)
     return dA, dB, db
@@ -259,16 +264,16 @@ def lsh_ffn_forward_fp8(X, x_scales, W1, w1_scales, b1, W2, w2_scales, b2, chunk
     tokens = X.numel() // d_model if d_model else 0
     d_ff = W1.shape[0] if isinstance(W1, torch.Tensor) and W1.dim() == 2 else -1
     mb, fb = _up(d_model, 128) // 128, _up(d_ff, 128) // 128
-    dev = _check((("X", X, X.shape, F8), ("x_scales", x_scales, (tokens, mb), f32),
+    dev = _check(("X", X, X.shape, F8), ("x_scales", x_scales, (tokens, mb), f32),
                   ("W1", W1, (d_ff, d_model), F8), ("w1_scales", w1_scales, (fb, mb), f32),
                   ("b1", b1, (d_ff,), bf), ("W2", W2, (d_model, d_ff), F8),
                   ("w2_scales", w2_scales, (mb, fb), f32), ("b2", b2, (d_model,), bf),
-                  ("Y", Y, X.shape, bf)))
+                  ("Y", Y, X.shape, bf))
     with _on(dev, stream):
         if Y is None:
             Y = torch.empty(X.shape, dtype=bf, device=dev)
         ws, wp, wn = _scratch("lsh_ffn_fp8_ws_size", (tokens, d_model, d_ff, chunk), ws, dev)
-        _go("lsh_ffn_forward_fp8", tokens, d_model, d_ff, chunk, X.data_ptr(),
+        _go("lsh_ffn_forward_fp8", dev, tokens, d_model, d_ff, chunk, X.data_ptr(),
             x_scales.data_ptr(), W1.data_ptr(), w1_scales.data_ptr(), b1.data_ptr(),
             W2.data_ptr(), w2_scales.data_ptr(), b2.data_ptr(), Y.data_ptr(), wp, wn)
     return Y
