@@ -29,8 +29,8 @@ template <typename XT, int kOut, int kNV, bool kWarp>
 lsh_status norm_fwd_go(const lsh::NormArgs& a, cudaStream_t st) {
   const long long per = kWarp ? lsh::kNormThreads / 32 : 1;
   const unsigned grid = (unsigned)((a.rows + per - 1) / per);
-  lsh::rmsnorm_fwd_kernel<XT, kOut, kNV, kWarp><<<grid, lsh::kNormThreads, 0, st>>>(a);
-  return last_launch();
+  return launch_pdl(lsh::rmsnorm_fwd_kernel<XT, kOut, kNV, kWarp>, dim3(grid),
+                    dim3(lsh::kNormThreads), 0, st, a);
 }
 template <typename XT, int kOut>
 lsh_status norm_fwd_launch(const lsh::NormArgs& a, cudaStream_t st) {
@@ -59,8 +59,8 @@ int norm_bwd_blocks(int32_t rows, int32_t cols) {
 
 template <typename XT, int kNV, bool kWarp>
 lsh_status norm_bwd_go(const lsh::NormBwdArgs& a, int blocks, cudaStream_t st) {
-  lsh::rmsnorm_bwd_kernel<XT, kNV, kWarp><<<(unsigned)blocks, lsh::kNormThreads, 0, st>>>(a);
-  return last_launch();
+  return launch_pdl(lsh::rmsnorm_bwd_kernel<XT, kNV, kWarp>, dim3((unsigned)blocks),
+                    dim3(lsh::kNormThreads), 0, st, a);
 }
 template <typename XT>
 lsh_status norm_bwd_launch(const lsh::NormBwdArgs& a, int blocks, cudaStream_t st) {
@@ -74,8 +74,8 @@ lsh_status norm_bwd_launch(const lsh::NormBwdArgs& a, int blocks, cudaStream_t s
 }
 
 lsh_status column_sum(const float* part, int blocks, int cols, float* out, cudaStream_t st) {
-  lsh::column_sum_kernel<<<(unsigned)ceil_div(cols, 32), 256, 0, st>>>(part, blocks, cols, out);
-  return last_launch();
+  return launch_pdl(lsh::column_sum_kernel, dim3((unsigned)ceil_div(cols, 32)), dim3(256), 0, st,
+                    part, blocks, cols, out);
 }
 
 template <typename XT>
@@ -84,16 +84,13 @@ lsh_status quant_launch(const lsh::QuantArgs& a, int block_rows, cudaStream_t st
     const long long padded = ((a.cols >> 3) + 15) & ~15;
     const long long grid = (a.rows * padded + 255) / 256;
     if (grid > 0x7fffffffLL) return LSH_ERR_UNSUPPORTED;
-    lsh::quant_rows_kernel<XT><<<(unsigned)grid, 256, 0, st>>>(a);
-    return last_launch();
+    return launch_pdl(lsh::quant_rows_kernel<XT>, dim3((unsigned)grid), dim3(256), 0, st, a);
   }
   const long long grid = ((a.rows + 127) / 128) * (long long)kblocks(a.cols);
   if (grid > 0x7fffffffLL) return LSH_ERR_UNSUPPORTED;
-  if (block_rows == 1)
-    lsh::quant_tile_kernel<XT, false><<<(unsigned)grid, 256, 0, st>>>(a);
-  else
-    lsh::quant_tile_kernel<XT, true><<<(unsigned)grid, 256, 0, st>>>(a);
-  return last_launch();
+  return launch_pdl(block_rows == 1 ? lsh::quant_tile_kernel<XT, false>
+                                    : lsh::quant_tile_kernel<XT, true>,
+                    dim3((unsigned)grid), dim3(256), 0, st, a);
 }
 
 lsh::QuantArgs quant_args(int32_t rows, int32_t cols, const void* X, void* Y, float* scales,

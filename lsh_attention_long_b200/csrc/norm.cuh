@@ -82,6 +82,8 @@ __device__ __forceinline__ void load8_any(const void* p, int is_bf16, size_t at,
 template <typename XT, int kOut, int kNV, bool kWarp>
 __global__ void __launch_bounds__(kNormThreads) rmsnorm_fwd_kernel(NormArgs a) {
   __shared__ float red[kNormThreads / 32];
+  grid_dep_wait();
+  grid_dep_launch();
   constexpr int kT = kWarp ? 32 : kNormThreads;  // threads of a row
   const int t = threadIdx.x & (kT - 1);
   const long long row = (long long)blockIdx.x * (kNormThreads / kT) + threadIdx.x / kT;
@@ -166,6 +168,8 @@ template <typename XT, int kNV, bool kWarp>
 __global__ void __launch_bounds__(kNormThreads) rmsnorm_bwd_kernel(NormBwdArgs a) {
   __shared__ float red[kNormThreads / 32];
   __shared__ float part[kWarp ? kNV * 256 : 1];
+  grid_dep_wait();
+  grid_dep_launch();
   constexpr int kT = kWarp ? 32 : kNormThreads;
   constexpr int kRows = kNormThreads / kT;  // rows in flight per block
   const int t = threadIdx.x & (kT - 1);
@@ -255,6 +259,8 @@ __global__ void __launch_bounds__(256) column_sum_kernel(const float* __restrict
                                                          int blocks, int cols,
                                                          float* __restrict__ out) {
   __shared__ float red[8][32];
+  grid_dep_wait();
+  grid_dep_launch();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float s = 0.f;

@@ -30,6 +30,8 @@ struct QuantArgs {
 template <typename XT>
 __global__ void __launch_bounds__(256) quant_rows_kernel(QuantArgs a) {
   constexpr bool kBf16 = sizeof(XT) == 2;
+  grid_dep_wait();
+  grid_dep_launch();
   const int pieces = a.cols >> 3;
   const int padded = (pieces + 15) & ~15;  // a row starts at lane 0 or 16
   const long long g = (long long)blockIdx.x * 256 + threadIdx.x;
@@ -55,18 +57,39 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(QuantArgs a) {
   if ((p & 15) == 0) a.scales[(size_t)row * (padded >> 4) + (p >> 4)] = am / kE4m3Max;
 }
 
+// Magnitudes of 8 rows over 16 lanes, m[i] being the lane's own of row i: the
+// largest of row (lane & 14) / 2, which the lane returns.  Each step hands half
+// of the rows to the lane across, so 8 shuffles do for 8 rows.
+__device__ __forceinline__ uint32_t rows_amax(uint32_t* m, int lane) {
+#pragma unroll
+  for (int h = 4; h; h >>= 1) {
+    const bool up = lane & (2 * h);
+#pragma unroll
+    for (int i = 0; i < h; ++i) {
+      const uint32_t give = up ? m[i] : m[i + h], keep = up ? m[i + h] : m[i];
+      m[i] = max(keep, __shfl_xor_sync(0xffffffffu, give, 2 * h));
+    }
+  }
+  return max(m[0], __shfl_xor_sync(0xffffffffu, m[0], 1));
+}
+
 // 256 threads; thread (rg, cg) = (tid / 16, tid % 16) holds rows 8 rg .. 8 rg
 // + 7 and columns 8 cg .. 8 cg + 7 of the tile, so a row block (1 x 128) lies
 // in 16 neighbouring lanes and a thread's part of the transposed tile is 8
 // pieces of 8 consecutive bytes.
+//
+// With some 14 instructions an entry the kernel is near the schedulers' limit
+// as well as memory's, so the two divisions of a block (its scale and the
+// scale's inverse) are one lane's, which hands the inverse on.
 template <typename XT, bool kSquare>
-__global__ void __launch_bounds__(256) quant_tile_kernel(QuantArgs a) {
+__global__ void __launch_bounds__(256, 2) quant_tile_kernel(QuantArgs a) {
   constexpr bool kBf16 = sizeof(XT) == 2;
   __shared__ uint32_t cmax[8][128];
   __shared__ float csum[8][128];
   __shared__ float cinv[128];
   __shared__ __align__(16) uint8_t tile[128 * 128];
-  const int tid = threadIdx.x, warp = tid >> 5, rg = tid >> 4, cg = tid & 15;
+  grid_dep_wait();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, rg = tid >> 4, cg = tid & 15;
   const int cb = (a.cols + 127) >> 7;
   const long long tr = blockIdx.x / cb;  // row block
   const int tc = (int)(blockIdx.x % cb); // column block
@@ -82,6 +105,7 @@ __global__ void __launch_bounds__(256) quant_tile_kernel(QuantArgs a) {
       for (int e = 0; e < 8; ++e) v[i][e] = 0.f;
     }
   }
+  grid_dep_launch();
   float inv_sq = 0.f;
   if (kSquare) {  // one maximum for the whole tile
     uint32_t m = 0;
@@ -91,7 +115,7 @@ __global__ void __launch_bounds__(256) quant_tile_kernel(QuantArgs a) {
       for (int e = 0; e < 8; ++e) m = max(m, mag_bits(v[i][e]));
 #pragma unroll
     for (int o = 16; o; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if ((tid & 31) == 0) cmax[warp][0] = m;
+    if (lane == 0) cmax[warp][0] = m;
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 8; ++i) m = max(m, cmax[i][0]);
@@ -104,27 +128,30 @@ __global__ void __launch_bounds__(256) quant_tile_kernel(QuantArgs a) {
     }
   }
   if (a.y) {
+    float inv_row = 0.f;  // of row (cg & 14) / 2
+    if (!kSquare) {
+      uint32_t m[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        m[i] = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m[i] = max(m[i], mag_bits(v[i][e]));
+      }
+      const float am = block_amax(rows_amax(m, lane));
+      inv_row = kE4m3Max / am;
+      const long long r = row0 + (cg >> 1);
+      if (!(cg & 1) && r < a.rows) a.scales[(size_t)r * cb + tc] = am / kE4m3Max;
+    }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      float inv = inv_sq;
-      if (!kSquare) {
-        uint32_t m = 0;
+      const float inv =
+          kSquare ? inv_sq : __shfl_sync(0xffffffffu, inv_row, (lane & 16) + 2 * i);
+      float q[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) m = max(m, mag_bits(v[i][e]));
-#pragma unroll
-        for (int o = 8; o; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const float am = block_amax(m);
-        inv = kE4m3Max / am;
-        if (cg == 0 && row0 + i < a.rows)
-          a.scales[(size_t)(row0 + i) * cb + tc] = am / kE4m3Max;
-      }
-      if (row0 + i < a.rows && col0 < a.cols) {
-        float q[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) q[e] = scale_to_e4m3<kBf16>(v[i][e], inv);
+      for (int e = 0; e < 8; ++e) q[e] = scale_to_e4m3<kBf16>(v[i][e], inv);
+      if (row0 + i < a.rows && col0 < a.cols)
         *reinterpret_cast<uint2*>(a.y + (size_t)(row0 + i) * a.cols + col0) =
             make_uint2(e4m3x4(q[0], q[1], q[2], q[3]), e4m3x4(q[4], q[5], q[6], q[7]));
-      }
     }
   }
   if (a.colsum) {
@@ -136,16 +163,8 @@ __global__ void __launch_bounds__(256) quant_tile_kernel(QuantArgs a) {
       s += __shfl_xor_sync(0xffffffffu, s, 16);
       if ((tid & 16) == 0) csum[warp][8 * cg + e] = s;
     }
-    __syncthreads();
-    if (tid < 128 && tc * 128 + tid < a.cols) {
-      float s = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) s += csum[i][tid];
-      a.colsum[(size_t)tr * a.cols + tc * 128 + tid] = s;
-    }
   }
-  if (!a.yt) return;
-  if (!kSquare) {
+  if (a.yt && !kSquare) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       uint32_t m = 0;
@@ -154,20 +173,30 @@ __global__ void __launch_bounds__(256) quant_tile_kernel(QuantArgs a) {
       m = max(m, __shfl_xor_sync(0xffffffffu, m, 16));
       if ((tid & 16) == 0) cmax[warp][8 * cg + e] = m;
     }
+  }
+  if (a.colsum || (a.yt && !kSquare)) {
     __syncthreads();
+    const int c = tc * 128 + (tid & 127);
     if (tid < 128) {
-      uint32_t m = 0;
+      if (a.yt && !kSquare) {
+        uint32_t m = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) m = max(m, cmax[i][tid]);
-      const float am = block_amax(m);
-      cinv[tid] = kE4m3Max / am;
-      const int c = tc * 128 + tid;
-      if (c < a.cols) a.scales_t[(size_t)c * ((a.rows + 127) >> 7) + tr] = am / kE4m3Max;
+        for (int i = 0; i < 8; ++i) m = max(m, cmax[i][tid]);
+        const float am = block_amax(m);
+        cinv[tid] = kE4m3Max / am;
+        if (c < a.cols) a.scales_t[(size_t)c * ((a.rows + 127) >> 7) + tr] = am / kE4m3Max;
+      }
+    } else if (a.colsum && c < a.cols) {
+      float s = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s += csum[i][tid & 127];
+      a.colsum[(size_t)tr * a.cols + c] = s;
     }
     __syncthreads();
   }
-  // row c of the transposed tile: 16 pieces of 8 bytes, piece rg at rg ^ (c >> 3)
-  // so that the 16 lanes of a store (one per column group) hit distinct banks
+  if (!a.yt) return;
+  // row c of the transposed tile: 16 pieces of 8 bytes, in pairs of pieces, so
+  // that a store's 16 lanes (one per column group) hit distinct banks
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     const int c = 8 * cg + e;
@@ -175,19 +204,19 @@ __global__ void __launch_bounds__(256) quant_tile_kernel(QuantArgs a) {
     float q[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) q[i] = scale_to_e4m3<kBf16>(v[i][e], inv);
-    *reinterpret_cast<uint2*>(tile + c * 128 + ((rg ^ cg) << 3)) =
+    *reinterpret_cast<uint2*>(tile + c * 128 + ((((rg >> 1) ^ (cg & 7)) << 4) | ((rg & 1) << 3))) =
         make_uint2(e4m3x4(q[0], q[1], q[2], q[3]), e4m3x4(q[4], q[5], q[6], q[7]));
   }
   __syncthreads();
-  // out: 16 lanes write a row's 128 bytes (pitch_t is a multiple of 16, so
-  // its end never cuts a piece)
-  const long long r = tr * 128 + 8 * (tid & 15);
+  // out: 8 lanes write a row's 128 bytes (pitch_t is a multiple of 16, so its
+  // end never cuts a piece)
+  const long long r = tr * 128 + 16 * (tid & 7);
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const int c = 16 * k + (tid >> 4);
+  for (int k = 0; k < 4; ++k) {
+    const int c = 32 * k + (tid >> 3);
     if (tc * 128 + c < a.cols && r < a.pitch_t)
-      *reinterpret_cast<uint2*>(a.yt + (size_t)(tc * 128 + c) * a.pitch_t + r) =
-          *reinterpret_cast<const uint2*>(tile + c * 128 + (((tid & 15) ^ (c >> 3)) << 3));
+      *reinterpret_cast<uint4*>(a.yt + (size_t)(tc * 128 + c) * a.pitch_t + r) =
+          *reinterpret_cast<const uint4*>(tile + c * 128 + (((tid & 7) ^ ((c >> 3) & 7)) << 4));
   }
 }
 
