@@ -396,8 +396,9 @@ LSH_API lsh_status lsh_matmul_fp8_backward(int32_t M, int32_t N, int32_t K, cons
  * W1 [d_ff, d_model] and W2 [d_model, d_ff] with 128 x 128 scales, b1, b2 and
  * Y bf16; q(.) is 1 x 128 blocks of the fp32 hidden activation.  `chunk`
  * positions at a time, a multiple of 128, so that the hidden activation exists
- * for one chunk only (in ws, at least lsh_ffn_fp8_ws_size() bytes); the chunk
- * does not change the result. */
+ * for two chunks at most, the one being made and the one being read (in ws, at
+ * least lsh_ffn_fp8_ws_size() bytes).  The chunk changes the result only
+ * through the order of the fp32 sums. */
 LSH_API size_t lsh_ffn_fp8_ws_size(int32_t tokens, int32_t d_model, int32_t d_ff, int32_t chunk);
 LSH_API lsh_status lsh_ffn_forward_fp8(int32_t tokens, int32_t d_model, int32_t d_ff,
                                        int32_t chunk, const void* X, const float* x_scales,

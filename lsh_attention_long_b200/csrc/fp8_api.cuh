@@ -211,23 +211,27 @@ lsh_status fp8_tc_gemm(const lsh::Fp8TcArgs& a, cudaStream_t st) {
 }
 
 // early_b: see Fp8SkinnyArgs.
-lsh_status fp8_gemm_launch(const lsh::Fp8GemmArgs& g, cudaStream_t st, int early_b = 0) {
+lsh_status fp8_gemm_launch(const lsh::Fp8GemmArgs& g, cudaStream_t st, int order = lsh::kF8Wait,
+                           int early_b = 0) {
   if (g.M <= lsh::kSkMaxM)
     return fp8_skinny_launch<lsh::kF8Store>(g, nullptr, nullptr, early_b, st);
   lsh::Fp8TcArgs a = {};
   a.g = g;
   a.wait_limit = g_wait_limit;
+  a.order = order;
   return g.b_rows == 1 ? fp8_tc_gemm<true>(a, st) : fp8_tc_gemm<false>(a, st);
 }
 
 // The hidden activation of the feed-forward: max(0, A B^T + bias) in 8 bits.
-lsh_status fp8_gemm_quant_launch(const lsh::Fp8GemmArgs& g, void* Q, float* qs, cudaStream_t st) {
+lsh_status fp8_gemm_quant_launch(const lsh::Fp8GemmArgs& g, void* Q, float* qs, int order,
+                                 cudaStream_t st) {
   if (g.M <= lsh::kSkMaxM) return fp8_skinny_launch<lsh::kF8Quant>(g, Q, qs, 0, st);
   lsh::Fp8TcArgs a = {};
   a.g = g;
   a.Q = static_cast<uint8_t*>(Q);
   a.qs = qs;
   a.wait_limit = g_wait_limit;
+  a.order = order;
   return fp8_pair_tiles(g) ? fp8_tc_launch<2, 256, lsh::kF8Quant, false, 1>(a, st)
                            : fp8_tc_launch<1, 128, lsh::kF8Quant, false, 1>(a, st);
 }
@@ -263,16 +267,26 @@ Fp8BwdLayout fp8_bwd_layout(int32_t M, int32_t N, int32_t K) {
   return l;
 }
 
-// Workspace of lsh_ffn_forward_fp8: one chunk's hidden activation.
+// Workspace of lsh_ffn_forward_fp8: the hidden activation of two chunks, so
+// that one chunk's can be made while the last one's is still read (of one,
+// where there is no more).
 struct Ffn8Layout {
-  size_t h8, s, total;
+  size_t h8[2], s[2], total;
 };
-Ffn8Layout ffn8_layout(int32_t rows, int32_t d_ff) {
+Ffn8Layout ffn8_layout(int32_t tokens, int32_t d_ff, int32_t chunk) {
   Ffn8Layout l;
   size_t off = 0;
   auto take = [&](size_t bytes) { const size_t at = off; off += align_up(bytes); return at; };
-  l.h8 = take((size_t)rows * d_ff);
-  l.s = take((size_t)rows * kblocks(d_ff) * sizeof(float));
+  const size_t rows = tokens < chunk ? tokens : chunk;
+  for (int i = 0; i < 2; ++i) {
+    if (i && tokens <= chunk) {
+      l.h8[1] = l.h8[0];
+      l.s[1] = l.s[0];
+      break;
+    }
+    l.h8[i] = take(rows * d_ff);
+    l.s[i] = take(rows * kblocks(d_ff) * sizeof(float));
+  }
   l.total = off;
   return l;
 }
@@ -436,7 +450,7 @@ lsh_status lsh_matmul_fp8_backward(int32_t M, int32_t N, int32_t K, const void* 
 
 size_t lsh_ffn_fp8_ws_size(int32_t tokens, int32_t d_model, int32_t d_ff, int32_t chunk) {
   if (ffn8_check(tokens, d_model, d_ff, chunk) != LSH_OK || tokens == 0) return 0;
-  return ffn8_layout(tokens < chunk ? tokens : chunk, d_ff).total;
+  return ffn8_layout(tokens, d_ff, chunk).total;
 }
 
 lsh_status lsh_ffn_forward_fp8(int32_t tokens, int32_t d_model, int32_t d_ff, int32_t chunk,
@@ -451,24 +465,47 @@ lsh_status lsh_ffn_forward_fp8(int32_t tokens, int32_t d_model, int32_t d_ff, in
     return LSH_ERR_INVALID_ARG;
   if (any_misaligned({X, x_scales, W1, w1_scales, b1, W2, w2_scales, b2, Y, ws}))
     return LSH_ERR_INVALID_ARG;
-  const Ffn8Layout l = ffn8_layout(tokens < chunk ? tokens : chunk, d_ff);
+  const Ffn8Layout l = ffn8_layout(tokens, d_ff, chunk);
   if (!ws || ws_bytes < l.total) return LSH_ERR_WORKSPACE;
   cudaStream_t st = as_stream(stream);
   char* w = static_cast<char*>(ws);
-  float* hs = reinterpret_cast<float*>(w + l.s);
-  for (int64_t c0 = 0; c0 < tokens; c0 += chunk) {
-    const int n = (int)(tokens - c0 < chunk ? tokens - c0 : chunk);
-    lsh::Fp8GemmArgs g1 = fp8_gemm_args(n, d_ff, d_model,
-                                        static_cast<const uint8_t*>(X) + c0 * d_model,
-                                        x_scales + c0 * kblocks(d_model), W1, w1_scales, 128);
-    g1.bias = static_cast<const __nv_bfloat16*>(b1);
-    if ((s = fp8_gemm_quant_launch(g1, w + l.h8, hs, st)) != LSH_OK) return s;
-    lsh::Fp8GemmArgs g2 = fp8_gemm_args(n, d_model, d_ff, w + l.h8, hs, W2, w2_scales, 128);
-    g2.bias = static_cast<const __nv_bfloat16*>(b2);
-    g2.C = static_cast<__nv_bfloat16*>(Y) + c0 * d_model;
-    // W2: complete before the hidden product's wait returned, which was
-    // before this launch could start
-    if ((s = fp8_gemm_launch(g2, st, 1)) != LSH_OK) return s;
+  const int64_t n_chunks = (tokens + (int64_t)chunk - 1) / chunk;
+  const auto rows_of = [&](int64_t c) {
+    return (int)(tokens - c * chunk < chunk ? tokens - c * chunk : chunk);
+  };
+  const auto hidden = [&](int64_t c) { return w + l.h8[c & 1]; };
+  const auto hidden_s = [&](int64_t c) { return reinterpret_cast<float*>(w + l.s[c & 1]); };
+  // up(c) makes chunk c's hidden activation, down(c) its output.  They go up(0),
+  // up(1), down(0), up(2), down(1), .., down(n - 1), so that each fills the SMs
+  // that the one before leaves idle at its end:
+  //   up(c + 1) loads inputs only; before its first store (into the buffer that
+  //   down(c - 1), just before it, reads) it waits for that grid, which had
+  //   itself waited for up(c) at its end; only then may down(c) start;
+  //   down(c) thus starts after up(c), and need not wait for up(c + 1).
+  // The last down has no up before it and waits at its start.  (A chunk of few
+  // rows takes the kernel for those, which always waits at its start.)
+  const auto up = [&](int64_t c) {
+    const int64_t c0 = c * chunk;
+    lsh::Fp8GemmArgs g = fp8_gemm_args(rows_of(c), d_ff, d_model,
+                                       static_cast<const uint8_t*>(X) + c0 * d_model,
+                                       x_scales + c0 * kblocks(d_model), W1, w1_scales, 128);
+    g.bias = static_cast<const __nv_bfloat16*>(b1);
+    g.relu = 1;
+    return fp8_gemm_quant_launch(g, hidden(c), hidden_s(c), c ? lsh::kF8Late : lsh::kF8Wait, st);
+  };
+  const auto down = [&](int64_t c) {
+    lsh::Fp8GemmArgs g = fp8_gemm_args(rows_of(c), d_model, d_ff, hidden(c), hidden_s(c), W2,
+                                       w2_scales, 128);
+    g.bias = static_cast<const __nv_bfloat16*>(b2);
+    g.C = static_cast<__nv_bfloat16*>(Y) + c * chunk * d_model;
+    // W2 was complete before the first up's wait returned, and so before this
+    // launch can start
+    return fp8_gemm_launch(g, st, c + 1 < n_chunks ? lsh::kF8End : lsh::kF8Wait, 1);
+  };
+  if ((s = up(0)) != LSH_OK) return s;
+  for (int64_t c = 0; c < n_chunks; ++c) {
+    if (c + 1 < n_chunks && (s = up(c + 1)) != LSH_OK) return s;
+    if ((s = down(c)) != LSH_OK) return s;
   }
   return LSH_OK;
 }

@@ -22,4 +22,11 @@ struct Fp8GemmArgs {
   int c_f32;                 // fp32, else bf16
 };
 
+// max(0, v); a NaN stays one.
+__device__ __forceinline__ float relu_nan(float v) {
+  float r;
+  asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(r) : "f"(v));
+  return r;
+}
+
 }  // namespace lsh

@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(32 * kW) gemm_fp8_skinny_kernel(Fp8SkinnyArgs 
 #pragma unroll
       for (int w = 0; w < kW; ++w) v[i] += red[w][r][m];
       if (g.bias) v[i] += __bfloat162float(g.bias[n]);
-      if (kEpi == kF8Quant || g.relu) v[i] = v[i] < 0.f ? 0.f : v[i];  // a NaN stays one
+      if (kEpi == kF8Quant || g.relu) v[i] = relu_nan(v[i]);
     }
   }
   if (kEpi == kF8Store) {

@@ -56,7 +56,15 @@ struct Fp8TcArgs {
   uint8_t* Q;      // kF8Quant: codes [M, N] of max(0, A B^T + bias)
   float* qs;       // and their 1 x 128 scales [M, ceil(N / 128)]
   long long wait_limit;
+  int order;  // Fp8Order
 };
+
+// How a grid follows the previous one in its stream (it may be scheduled while
+// that one finishes).  kF8Wait: waits for its end before any access.  The other
+// two load nothing that the previous grid writes, nor any that may still run.
+// kF8Late: waits before its first store, and only then lets the next grid
+// start.  kF8End: waits at its own end, so that this is the previous one's too.
+enum Fp8Order { kF8Wait = 0, kF8Late = 1, kF8End = 2 };
 
 template <int kPair, int kBN, int kEpi, bool kColScale>
 struct Fp8Cfg {
@@ -68,7 +76,7 @@ struct Fp8Cfg {
   static constexpr int kOutBoxes = kEpi == kF8Quant ? 1 : kCols / 64;
   static constexpr int kOutBytes = 8 * kOutBoxes * 4096;
   static constexpr int kScaleBytes =
-      kF8Slots * 4 * 4 * (kColScale ? kF8BM + kBN : 2 * kF8BM);
+      kF8Slots * 4 * 4 * (kColScale ? kF8BM + kBN : 2 * kF8BM) + 4 * kBN * 4;
   static constexpr int kStages =  // what is left of 227 KB, less alignment and barriers
       (232448 - 1024 - 512 - kOutBytes - kScaleBytes) / (kABytes + kBBytes);
 };
@@ -80,6 +88,8 @@ struct Fp8Smem {
   // row sa * sb, or (b_rows 1) per row sa and per column sb
   float4 rs[kF8Slots][kColScale ? 1 : 2][kF8BM];
   float cs[kColScale ? kF8Slots : 1][4][kColScale ? kBN : 1];
+  // the tile's bias, by tile: the scales' warp is at most two tiles ahead
+  float4 bias[4][kBN / 4];
   uint64_t full[C::kStages], empty[C::kStages];
   uint64_t acc_full[C::kBufs], acc_empty[C::kBufs];
   uint64_t sc_full[kF8Slots], sc_empty[kF8Slots];
@@ -180,8 +190,8 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   else
     __syncthreads();
   tc::fence_after_sync();
-  grid_dep_wait();
-  grid_dep_launch();
+  if (a.order == kF8Wait) grid_dep_wait();
+  if (a.order != kF8Late) grid_dep_launch();
   const uint32_t tmem = S.tmem_base;
   const auto commit = [](uint64_t* bar) { kPair == 2 ? tc::mma_commit_pair(bar) : tc::mma_commit(bar); };
   const int n_n = (g.N + kBN - 1) / kBN;
@@ -286,22 +296,22 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     // Lane t has rows t, t + 32, .. (and columns t, t + 32, ..); four blocks'
     // scales are in flight at once.
     constexpr int kC = kColScale ? kBN / 32 : 2;
-    uint32_t q = 0;
+    uint32_t q = 0, tile = 0;
     bool ok = true;
-    for (int u = first_unit; u < n_units && ok; u += unit_step) {
+    for (int u = first_unit; u < n_units && ok; u += unit_step, ++tile) {
       const int m0 = (u / n_n * kPair + rank) * kF8BM, n0 = (u % n_n) * kBN;
-      // past the ends every code is zero, and any row's scale will do
+      // past the ends every code is zero, and the last row's scale will do
       const float* pa[4];
       const float* pb[kC];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int r = m0 + lane + 32 * i;
-        pa[i] = g.sa + (size_t)(r < g.M ? r : 0) * k_all + k_lo;
+        pa[i] = g.sa + (size_t)(r < g.M ? r : g.M - 1) * k_all + k_lo;
       }
 #pragma unroll
       for (int i = 0; i < kC; ++i) {
         const int n = kColScale ? n0 + lane + 32 * i : n0 + i * kCols;
-        pb[i] = g.sb + (size_t)(n < g.N ? (kColScale ? n : n / g.b_rows) : 0) * k_all + k_lo;
+        pb[i] = g.sb + (size_t)((n < g.N ? n : g.N - 1) / (kColScale ? 1 : g.b_rows)) * k_all + k_lo;
       }
       for (int kb = 0; kb < n_k && ok; kb += 4, ++q) {
         float va[4][4], vb[kC][4];
@@ -314,9 +324,27 @@ __global__ void __launch_bounds__(kF8Threads, 1)
           for (int i = 0; i < kC; ++i) vb[i][j] = pb[i][k];
         }
         const int slot = q % kF8Slots;
+        float4 bias[kBN / 128];
+        if (kb == 0 && g.bias) {
+#pragma unroll
+          for (int i = 0; i < kBN / 128; ++i) {
+            const int n = n0 + 4 * (lane + 32 * i);
+            bias[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (n < g.N) {
+              const uint2 bv = *reinterpret_cast<const uint2*>(g.bias + n);
+              const float2 lo = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&bv.x));
+              const float2 hi = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&bv.y));
+              bias[i] = make_float4(lo.x, lo.y, hi.x, hi.y);
+            }
+          }
+        }
         ok = f8_wait(&S.sc_empty[slot], ((q / kF8Slots) & 1u) ^ 1u, &S.abort, limit);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
+        if (kb == 0 && g.bias) {
+#pragma unroll
+          for (int i = 0; i < kBN / 128; ++i) S.bias[tile % 4][lane + 32 * i] = bias[i];
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           if (kColScale) {
@@ -351,9 +379,9 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     uint32_t free_bar = tc::smem_u32(&S.acc_empty[0]);
     if (kPair == 2) free_bar = tc::cluster_map(free_bar, 0);
     const uint32_t lane_base = tmem + ((uint32_t)(sub * 32) << 16) + half * kCols;
-    uint32_t q = 0, qs = 0;
+    uint32_t q = 0, qs = 0, tile = 0;
     bool ok = true;
-    for (int u = first_unit; u < n_units; u += unit_step) {
+    for (int u = first_unit; u < n_units; u += unit_step, ++tile) {
       const int m0 = (u / n_n * kPair + rank) * kF8BM, c0 = (u % n_n) * kBN + half * kCols;
       float acc[kCols];
 #pragma unroll
@@ -414,6 +442,10 @@ __global__ void __launch_bounds__(kF8Threads, 1)
         __syncwarp();
         tc::mbar_arrive_if(tc::smem_u32(&S.sc_empty[slot]), lane == 0);  // its scales are read
       }
+      if (a.order == kF8Late && tile == 0) {
+        grid_dep_wait();
+        grid_dep_launch();
+      }
       const bool bad = f8_any(!ok);  // for all of them, or none
       if (bad && !kSplit) break;
       if (kSplit) {
@@ -445,14 +477,12 @@ __global__ void __launch_bounds__(kF8Threads, 1)
               o[0] += x.x; o[1] += x.y; o[2] += x.z; o[3] += x.w;
             }
             if (g.bias) {
-              const uint2 bv = *reinterpret_cast<const uint2*>(g.bias + c);
-              const float2 lo = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&bv.x));
-              const float2 hi = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&bv.y));
-              o[0] += lo.x; o[1] += lo.y; o[2] += hi.x; o[3] += hi.y;
+              const float4 t = S.bias[0][half * (kCols / 4) + part * kW4 + j];
+              o[0] += t.x; o[1] += t.y; o[2] += t.z; o[3] += t.w;
             }
             if (g.relu) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i) o[i] = o[i] < 0.f ? 0.f : o[i];  // a NaN stays one
+              for (int i = 0; i < 4; ++i) o[i] = relu_nan(o[i]);
             }
             if (g.c_f32)
               *reinterpret_cast<float4*>(static_cast<float*>(g.C) + (size_t)row * g.N + c) =
@@ -483,26 +513,25 @@ __global__ void __launch_bounds__(kF8Threads, 1)
         __syncwarp();
       };
       if (g.bias) {
+        const float4* bias = S.bias[tile % 4] + half * (kCols / 4);
 #pragma unroll
-        for (int e = 0; e < kCols; e += 8) {
-          if (c0 + e < g.N) {
-            float bv[8];
-            load8(g.bias + c0 + e, bv);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) acc[e + i] += bv[i];
-          }
+        for (int e = 0; e < kCols; e += 4) {
+          const float4 t = bias[e / 4];
+          acc[e] += t.x; acc[e + 1] += t.y; acc[e + 2] += t.z; acc[e + 3] += t.w;
         }
       }
       if (kEpi == kF8Quant || g.relu) {
 #pragma unroll
-        for (int e = 0; e < kCols; ++e) acc[e] = acc[e] < 0.f ? 0.f : acc[e];  // a NaN stays one
+        for (int e = 0; e < kCols; ++e) acc[e] = relu_nan(acc[e]);
       }
       if (kEpi == kF8Quant) {
+        // (columns past N add nothing: they are sums of zeros, or NaN with the
+        // rest of their block)
         // a block is the thread's 128 columns, or (kBN = 128) its 64 and those
         // of the other warpgroup's thread of the same row
         uint32_t m = 0;
 #pragma unroll
-        for (int e = 0; e < kCols; ++e) m = max(m, c0 + e < g.N ? mag_bits(acc[e]) : 0u);
+        for (int e = 0; e < kCols; ++e) m = max(m, __float_as_uint(acc[e]));  // none is negative
         if (kCols == 64) {
           S.amax[half][et] = m;
           asm volatile("bar.sync 1, 256;" ::: "memory");
@@ -554,6 +583,8 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     if (lane == 0) tc::bulk_wait();
     __syncwarp();
   }
+  // so that this grid's end is also the previous one's, whoever waits for it
+  if (a.order == kF8End) grid_dep_wait();
   if (kSplit && warp < 4) {  // the epilogue's two
     __syncwarp();
     tc::cluster_sync();

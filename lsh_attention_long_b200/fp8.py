@@ -248,7 +248,7 @@ def lsh_matmul_fp8_backward(dC, A, Bt, bt_scales, *, out_dtype=torch.bfloat16, d
 
 
 def ffn_fp8_workspace(tokens: int, d_model: int, d_ff: int, chunk: int, device) -> torch.Tensor:
-    """Device scratch for lsh_ffn_forward_fp8: one chunk's hidden activation."""
+    """Device scratch for lsh_ffn_forward_fp8: the hidden activation of two chunks."""
     n = load_library().lsh_ffn_fp8_ws_size(tokens, d_model, d_ff, chunk)
     return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
 

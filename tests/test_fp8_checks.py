@@ -153,5 +153,7 @@ def test_feed_forward_abi(lib):
     need = lib.lsh_ffn_fp8_ws_size(4, 64, 128, 128)
     assert need > 0 and ffn(n=need - 1) == WORKSPACE and ffn(ws=None) == WORKSPACE
     assert ffn(T=0, X=None, ws=None) == OK and lib.lsh_ffn_fp8_ws_size(0, 64, 128, 128) == 0
-    # one chunk's hidden activation: no more than one chunk's worth
-    assert lib.lsh_ffn_fp8_ws_size(1 << 20, 64, 128, 128) == lib.lsh_ffn_fp8_ws_size(128, 64, 128, 128)
+    # the hidden activation of two chunks, however many there are
+    one = lib.lsh_ffn_fp8_ws_size(128, 64, 128, 128)
+    assert lib.lsh_ffn_fp8_ws_size(129, 64, 128, 128) == 2 * one
+    assert lib.lsh_ffn_fp8_ws_size(1 << 20, 64, 128, 128) == 2 * one
