@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(kNormThreads) rmsnorm_fwd_kernel(NormArgs a) {
 template <typename XT, int kNV, bool kWarp>
 __global__ void __launch_bounds__(kNormThreads) rmsnorm_bwd_kernel(NormBwdArgs a) {
   __shared__ float red[kNormThreads / 32];
-  __shared__ float part[kWarp ? kNV * 256 : 1];
+  __shared__ float part[kWarp ? kNormThreads / 32 : 1][kWarp ? kNV * 256 : 1];
   grid_dep_wait();
   grid_dep_launch();
   constexpr int kT = kWarp ? 32 : kNormThreads;
@@ -230,20 +230,15 @@ __global__ void __launch_bounds__(kNormThreads) rmsnorm_bwd_kernel(NormBwdArgs a
     }
   }
   if (kWarp) {  // the warps' sums, added in order of warp
-    for (int wi = 0; wi < kNormThreads / 32; ++wi) {
-      if ((int)(threadIdx.x >> 5) == wi) {
 #pragma unroll
-        for (int i = 0; i < kNV; ++i)
+    for (int i = 0; i < kNV; ++i) store8(part[threadIdx.x >> 5] + 8 * (t + i * 32), dw[i]);
+    __syncthreads();
+    for (int c = threadIdx.x; c < a.cols; c += kNormThreads) {
+      float s = 0.f;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            float* s = part + 8 * (t + i * 32) + e;
-            *s = wi ? *s + dw[i][e] : dw[i][e];
-          }
-      }
-      __syncthreads();
+      for (int i = 0; i < kNormThreads / 32; ++i) s += part[kWarp ? i : 0][kWarp ? c : 0];
+      a.dw[(size_t)blockIdx.x * a.cols + c] = s;
     }
-    for (int c = threadIdx.x; c < a.cols; c += kNormThreads)
-      a.dw[(size_t)blockIdx.x * a.cols + c] = part[c];
   } else {
 #pragma unroll
     for (int i = 0; i < kNV; ++i) {

@@ -73,18 +73,72 @@ __device__ __forceinline__ uint32_t rows_amax(uint32_t* m, int lane) {
   return max(m[0], __shfl_xor_sync(0xffffffffu, m[0], 1));
 }
 
+// Eight neighbouring entries of a row as loaded: bf16 pairs stay packed (half
+// the registers, and magnitudes compare two at a time), fp32 as it is.
+template <typename XT>
+struct QuantPiece;
+template <>
+struct QuantPiece<__nv_bfloat16> {
+  uint32_t w[4];
+  static constexpr int kMags = 4;  // words of magnitudes, two columns each
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(p);
+  }
+  __device__ __forceinline__ void zero() { w[0] = w[1] = w[2] = w[3] = 0; }
+  __device__ __forceinline__ float get(int e) const {
+    return __uint_as_float((e & 1) ? w[e >> 1] & 0xffff0000u : w[e >> 1] << 16);
+  }
+  __device__ __forceinline__ uint32_t mag(int i) const { return w[i] & 0x7fff7fffu; }
+  // the larger magnitudes of two words (a NaN is the largest)
+  __device__ __forceinline__ static uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
+  // fp32 bits of a column's magnitude in its word
+  __device__ __forceinline__ static uint32_t column(uint32_t m, int e) {
+    return (e & 1) ? m & 0xffff0000u : m << 16;
+  }
+  __device__ __forceinline__ uint32_t amax() const {
+    const uint32_t m = max2(max2(mag(0), mag(1)), max2(mag(2), mag(3)));
+    return max(column(m, 0), column(m, 1));
+  }
+};
+template <>
+struct QuantPiece<float> {
+  float v[8];
+  static constexpr int kMags = 8;
+  __device__ __forceinline__ void load(const float* p) { load8(p, v); }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = 0.f;
+  }
+  __device__ __forceinline__ float get(int e) const { return v[e]; }
+  __device__ __forceinline__ uint32_t mag(int i) const { return mag_bits(v[i]); }
+  __device__ __forceinline__ static uint32_t max2(uint32_t a, uint32_t b) { return max(a, b); }
+  __device__ __forceinline__ static uint32_t column(uint32_t m, int) { return m; }
+  __device__ __forceinline__ uint32_t amax() const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = max(m, mag(e));
+    return m;
+  }
+};
+
 // 256 threads; thread (rg, cg) = (tid / 16, tid % 16) holds rows 8 rg .. 8 rg
 // + 7 and columns 8 cg .. 8 cg + 7 of the tile, so a row block (1 x 128) lies
 // in 16 neighbouring lanes and a thread's part of the transposed tile is 8
 // pieces of 8 consecutive bytes.
 //
-// With some 14 instructions an entry the kernel is near the schedulers' limit
-// as well as memory's, so the two divisions of a block (its scale and the
-// scale's inverse) are one lane's, which hands the inverse on.
+// The kernel is near the schedulers' limit as well as memory's, so the two
+// divisions of a block (its scale and the scale's inverse) are one lane's,
+// which hands the inverse on, and bf16 entries stay packed.
 template <typename XT, bool kSquare>
-__global__ void __launch_bounds__(256, 2) quant_tile_kernel(QuantArgs a) {
+__global__ void __launch_bounds__(256, sizeof(XT) == 2 ? 4 : 2) quant_tile_kernel(QuantArgs a) {
   constexpr bool kBf16 = sizeof(XT) == 2;
-  __shared__ uint32_t cmax[8][128];
+  using Piece = QuantPiece<XT>;
+  constexpr int kMags = Piece::kMags, kPerMag = 8 / kMags;
+  __shared__ uint32_t cmax[8][128 / kPerMag];
   __shared__ float csum[8][128];
   __shared__ float cinv[128];
   __shared__ __align__(16) uint8_t tile[128 * 128];
@@ -95,24 +149,20 @@ __global__ void __launch_bounds__(256, 2) quant_tile_kernel(QuantArgs a) {
   const int tc = (int)(blockIdx.x % cb); // column block
   const long long row0 = tr * 128 + 8 * rg;
   const int col0 = tc * 128 + 8 * cg;
-  float v[8][8];
+  Piece v[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    if (row0 + i < a.rows && col0 < a.cols) {
-      load8(static_cast<const XT*>(a.x) + (size_t)(row0 + i) * a.cols + col0, v[i]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[i][e] = 0.f;
-    }
+    if (row0 + i < a.rows && col0 < a.cols)
+      v[i].load(static_cast<const XT*>(a.x) + (size_t)(row0 + i) * a.cols + col0);
+    else
+      v[i].zero();
   }
   grid_dep_launch();
   float inv_sq = 0.f;
   if (kSquare) {  // one maximum for the whole tile
     uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) m = max(m, mag_bits(v[i][e]));
+    for (int i = 0; i < 8; ++i) m = max(m, v[i].amax());
 #pragma unroll
     for (int o = 16; o; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
     if (lane == 0) cmax[warp][0] = m;
@@ -132,11 +182,7 @@ __global__ void __launch_bounds__(256, 2) quant_tile_kernel(QuantArgs a) {
     if (!kSquare) {
       uint32_t m[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        m[i] = 0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) m[i] = max(m[i], mag_bits(v[i][e]));
-      }
+      for (int i = 0; i < 8; ++i) m[i] = v[i].amax();
       const float am = block_amax(rows_amax(m, lane));
       inv_row = kE4m3Max / am;
       const long long r = row0 + (cg >> 1);
@@ -148,7 +194,7 @@ __global__ void __launch_bounds__(256, 2) quant_tile_kernel(QuantArgs a) {
           kSquare ? inv_sq : __shfl_sync(0xffffffffu, inv_row, (lane & 16) + 2 * i);
       float q[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) q[e] = scale_to_e4m3<kBf16>(v[i][e], inv);
+      for (int e = 0; e < 8; ++e) q[e] = scale_to_e4m3<kBf16>(v[i].get(e), inv);
       if (row0 + i < a.rows && col0 < a.cols)
         *reinterpret_cast<uint2*>(a.y + (size_t)(row0 + i) * a.cols + col0) =
             make_uint2(e4m3x4(q[0], q[1], q[2], q[3]), e4m3x4(q[4], q[5], q[6], q[7]));
@@ -159,19 +205,19 @@ __global__ void __launch_bounds__(256, 2) quant_tile_kernel(QuantArgs a) {
     for (int e = 0; e < 8; ++e) {
       float s = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s += v[i][e];
+      for (int i = 0; i < 8; ++i) s += v[i].get(e);
       s += __shfl_xor_sync(0xffffffffu, s, 16);
       if ((tid & 16) == 0) csum[warp][8 * cg + e] = s;
     }
   }
   if (a.yt && !kSquare) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      uint32_t m = 0;
+    for (int e = 0; e < kMags; ++e) {
+      uint32_t m = v[0].mag(e);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) m = max(m, mag_bits(v[i][e]));
-      m = max(m, __shfl_xor_sync(0xffffffffu, m, 16));
-      if ((tid & 16) == 0) cmax[warp][8 * cg + e] = m;
+      for (int i = 1; i < 8; ++i) m = Piece::max2(m, v[i].mag(e));
+      m = Piece::max2(m, __shfl_xor_sync(0xffffffffu, m, 16));
+      if ((tid & 16) == 0) cmax[warp][kMags * cg + e] = m;
     }
   }
   if (a.colsum || (a.yt && !kSquare)) {
@@ -179,10 +225,10 @@ __global__ void __launch_bounds__(256, 2) quant_tile_kernel(QuantArgs a) {
     const int c = tc * 128 + (tid & 127);
     if (tid < 128) {
       if (a.yt && !kSquare) {
-        uint32_t m = 0;
+        uint32_t m = cmax[0][tid / kPerMag];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m = max(m, cmax[i][tid]);
-        const float am = block_amax(m);
+        for (int i = 1; i < 8; ++i) m = Piece::max2(m, cmax[i][tid / kPerMag]);
+        const float am = block_amax(Piece::column(m, tid));
         cinv[tid] = kE4m3Max / am;
         if (c < a.cols) a.scales_t[(size_t)c * ((a.rows + 127) >> 7) + tr] = am / kE4m3Max;
       }
@@ -203,7 +249,7 @@ __global__ void __launch_bounds__(256, 2) quant_tile_kernel(QuantArgs a) {
     const float inv = kSquare ? inv_sq : cinv[c];
     float q[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = scale_to_e4m3<kBf16>(v[i][e], inv);
+    for (int i = 0; i < 8; ++i) q[i] = scale_to_e4m3<kBf16>(v[i].get(e), inv);
     *reinterpret_cast<uint2*>(tile + c * 128 + ((((rg >> 1) ^ (cg & 7)) << 4) | ((rg & 1) << 3))) =
         make_uint2(e4m3x4(q[0], q[1], q[2], q[3]), e4m3x4(q[4], q[5], q[6], q[7]));
   }
