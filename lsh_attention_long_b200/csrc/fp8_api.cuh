@@ -25,22 +25,21 @@ lsh_status norm_check(int32_t rows, int32_t cols) {
   return LSH_OK;
 }
 
-template <typename XT, int kOut, int kNV, bool kWarp>
+template <typename XT, int kOut, int kNV, int kT>
 lsh_status norm_fwd_go(const lsh::NormArgs& a, cudaStream_t st) {
-  const long long per = kWarp ? lsh::kNormThreads / 32 : 1;
-  const unsigned grid = (unsigned)((a.rows + per - 1) / per);
-  return launch_pdl(lsh::rmsnorm_fwd_kernel<XT, kOut, kNV, kWarp>, dim3(grid),
-                    dim3(lsh::kNormThreads), 0, st, a);
+  constexpr int kBlock = lsh::norm_block(kT);
+  return launch_pdl(lsh::rmsnorm_fwd_kernel<XT, kOut, kNV, kT>,
+                    dim3((unsigned)ceil_div(a.rows, kBlock / kT)), dim3(kBlock), 0, st, a);
 }
 template <typename XT, int kOut>
 lsh_status norm_fwd_launch(const lsh::NormArgs& a, cudaStream_t st) {
-  if (a.cols <= 256) return norm_fwd_go<XT, kOut, 1, true>(a, st);
-  if (a.cols <= 512) return norm_fwd_go<XT, kOut, 2, true>(a, st);
-  if (a.cols <= 1024) return norm_fwd_go<XT, kOut, 4, true>(a, st);
-  if (a.cols <= 2048) return norm_fwd_go<XT, kOut, 1, false>(a, st);
-  if (a.cols <= 4096) return norm_fwd_go<XT, kOut, 2, false>(a, st);
-  if (a.cols <= 8192) return norm_fwd_go<XT, kOut, 4, false>(a, st);
-  return norm_fwd_go<XT, kOut, 8, false>(a, st);
+  if (a.cols <= 256) return norm_fwd_go<XT, kOut, 1, 32>(a, st);
+  if (a.cols <= 512) return norm_fwd_go<XT, kOut, 2, 32>(a, st);
+  if (a.cols <= 1024) return norm_fwd_go<XT, kOut, 4, 32>(a, st);
+  if (a.cols <= 2048) return norm_fwd_go<XT, kOut, 1, 256>(a, st);
+  if (a.cols <= 4096) return norm_fwd_go<XT, kOut, 2, 256>(a, st);
+  if (a.cols <= 8192) return norm_fwd_go<XT, kOut, 2, 512>(a, st);
+  return norm_fwd_go<XT, kOut, 2, 1024>(a, st);
 }
 template <typename XT>
 lsh_status norm_fwd_launch(const lsh::NormArgs& a, int y_dtype, cudaStream_t st) {
@@ -49,32 +48,41 @@ lsh_status norm_fwd_launch(const lsh::NormArgs& a, int y_dtype, cudaStream_t st)
   return norm_fwd_launch<XT, lsh::kNormF32>(a, st);
 }
 
-// Blocks of the backward: each leaves one partial row of dw.
-constexpr int kNormBwdBlocks = 592;
-int norm_bwd_blocks(int32_t rows, int32_t cols) {
-  const int per = cols <= lsh::kNormWarpCols ? lsh::kNormThreads / 32 : 1;
-  const int n = ceil_div(rows, per);
-  return n < kNormBwdBlocks ? n : kNormBwdBlocks;
+// Most blocks of the backward, each of which leaves one partial row of dw.
+int norm_bwd_most(int32_t rows, int32_t cols) {
+  const int n = ceil_div(rows, cols <= lsh::kNormWarpCols ? 8 : 1);
+  return n < 592 ? n : 592;
 }
 
-template <typename XT, int kNV, bool kWarp>
-lsh_status norm_bwd_go(const lsh::NormBwdArgs& a, int blocks, cudaStream_t st) {
-  return launch_pdl(lsh::rmsnorm_bwd_kernel<XT, kNV, kWarp>, dim3((unsigned)blocks),
-                    dim3(lsh::kNormThreads), 0, st, a);
+// The blocks loop over rows: as many as the SMs hold at once (a few more would
+// run alone at the end).
+template <typename XT, int kNV, int kT>
+lsh_status norm_bwd_go(const lsh::NormBwdArgs& a, int* blocks, cudaStream_t st) {
+  const auto kernel = lsh::rmsnorm_bwd_kernel<XT, kNV, kT>;
+  static const int per_sm = [&] {
+    int n = 0;
+    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, lsh::norm_block(kT), 0) ==
+                       cudaSuccess && n > 0
+               ? n
+               : 1;
+  }();
+  const int fit = per_sm * num_sms();
+  *blocks = *blocks < fit ? *blocks : fit;
+  return launch_pdl(kernel, dim3((unsigned)*blocks), dim3(lsh::norm_block(kT)), 0, st, a);
 }
 template <typename XT>
-lsh_status norm_bwd_launch(const lsh::NormBwdArgs& a, int blocks, cudaStream_t st) {
-  if (a.cols <= 256) return norm_bwd_go<XT, 1, true>(a, blocks, st);
-  if (a.cols <= 512) return norm_bwd_go<XT, 2, true>(a, blocks, st);
-  if (a.cols <= 1024) return norm_bwd_go<XT, 4, true>(a, blocks, st);
-  if (a.cols <= 2048) return norm_bwd_go<XT, 1, false>(a, blocks, st);
-  if (a.cols <= 4096) return norm_bwd_go<XT, 2, false>(a, blocks, st);
-  if (a.cols <= 8192) return norm_bwd_go<XT, 4, false>(a, blocks, st);
-  return norm_bwd_go<XT, 8, false>(a, blocks, st);
+lsh_status norm_bwd_launch(const lsh::NormBwdArgs& a, int* blocks, cudaStream_t st) {
+  if (a.cols <= 256) return norm_bwd_go<XT, 1, 32>(a, blocks, st);
+  if (a.cols <= 512) return norm_bwd_go<XT, 2, 32>(a, blocks, st);
+  if (a.cols <= 1024) return norm_bwd_go<XT, 4, 32>(a, blocks, st);
+  if (a.cols <= 2048) return norm_bwd_go<XT, 1, 256>(a, blocks, st);
+  if (a.cols <= 4096) return norm_bwd_go<XT, 1, 512>(a, blocks, st);
+  if (a.cols <= 8192) return norm_bwd_go<XT, 1, 1024>(a, blocks, st);
+  return norm_bwd_go<XT, 2, 1024>(a, blocks, st);
 }
 
 lsh_status column_sum(const float* part, int blocks, int cols, float* out, cudaStream_t st) {
-  return launch_pdl(lsh::column_sum_kernel, dim3((unsigned)ceil_div(cols, 32)), dim3(256), 0, st,
+  return launch_pdl(lsh::column_sum_kernel, dim3((unsigned)ceil_div(cols, 32)), dim3(1024), 0, st,
                     part, blocks, cols, out);
 }
 
@@ -326,7 +334,7 @@ lsh_status lsh_rmsnorm_forward(int32_t rows, int32_t cols, int32_t x_dtype, int3
 
 size_t lsh_rmsnorm_bwd_ws_size(int32_t rows, int32_t cols) {
   if (norm_check(rows, cols) != LSH_OK || rows == 0) return 0;
-  const int blocks = norm_bwd_blocks(rows, cols);
+  const int blocks = norm_bwd_most(rows, cols);
   return blocks > 1 ? align_up((size_t)blocks * cols * sizeof(float)) : 0;
 }
 
@@ -352,9 +360,9 @@ lsh_status lsh_rmsnorm_backward(int32_t rows, int32_t cols, int32_t x_dtype, int
   a.dy_bf16 = dy_dtype == LSH_BF16; a.w_bf16 = w_dtype == LSH_BF16;
   a.dy = dY; a.h = H; a.w = w; a.rstd = rstd; a.dh = dH; a.dx = dX;
   a.dw = need ? static_cast<float*>(ws) : dw;
-  const int blocks = norm_bwd_blocks(rows, cols);
-  s = x_dtype == LSH_BF16 ? norm_bwd_launch<__nv_bfloat16>(a, blocks, st)
-                          : norm_bwd_launch<float>(a, blocks, st);
+  int blocks = norm_bwd_most(rows, cols);
+  s = x_dtype == LSH_BF16 ? norm_bwd_launch<__nv_bfloat16>(a, &blocks, st)
+                          : norm_bwd_launch<float>(a, &blocks, st);
   if (s != LSH_OK || !need) return s;
   return column_sum(a.dw, blocks, cols, dw, st);
 }
