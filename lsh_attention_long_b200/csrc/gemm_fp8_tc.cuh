@@ -41,10 +41,15 @@
 namespace lsh {
 
 constexpr int kF8Threads = 384;
-// Registers: 168 a thread at launch (what 384 threads can have), of which the
-// first warpgroup gives up 96, and each epilogue thread gets 48 more.
-constexpr int kF8Regs = 168, kF8RegsLow = 72, kF8RegsHigh = 216;
-static_assert(128 * kF8RegsLow + 256 * kF8RegsHigh == kF8Threads * kF8Regs, "register split");
+// Registers: 168 a thread at launch (what 384 threads can have).  The first
+// warpgroup gives some up, twice as many warps share them: to each epilogue
+// thread 56 more, or 40 where the scales' warp (which holds a tile's column
+// scales too) needs its own.
+constexpr int kF8Regs = 168;
+__host__ __device__ constexpr int f8_regs_low(bool col_scale) { return col_scale ? 88 : 56; }
+__host__ __device__ constexpr int f8_regs_high(bool col_scale) {
+  return kF8Regs + (kF8Regs - f8_regs_low(col_scale)) / 2;
+}
 constexpr int kF8BM = 128, kF8BK = 128;
 
 constexpr int kF8Slots = 2;  // ring of scales, in four blocks of K
@@ -200,7 +205,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   const int k_lo = kSplit ? part * k_all / kParts : 0;
   const int n_k = kSplit ? (part + 1) * k_all / kParts - k_lo : k_all;
 
-  if (warp < 4) tc::reg_dec<kF8RegsLow>();
+  if (warp < 4) tc::reg_dec<f8_regs_low(kColScale)>();
   if (warp == 0) {
     // ------------------------------------------------------------ TMA loads
     if (lane == 0) {
@@ -368,7 +373,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     }
   } else {
     // ------------------------------------------------------------ epilogue
-    tc::reg_inc<kF8RegsHigh>();
+    tc::reg_inc<f8_regs_high(kColScale)>();
     const int sub = warp & 3;          // TMEM lanes 32 * sub .. 32 * sub + 31
     const int half = (warp - 4) >> 2;  // which half of the tile's columns
     const int et = (sub << 5) | lane;  // row in the tile
@@ -393,11 +398,12 @@ __global__ void __launch_bounds__(kF8Threads, 1)
         ok &= f8_wait(&S.sc_full[slot], (qs / kF8Slots) & 1u, &S.abort, limit);
         const float4 s4 = S.rs[slot][kColScale ? 0 : half][et];
         const float sj[4] = {s4.x, s4.y, s4.z, s4.w};
-#pragma unroll
+        // (unrolled twice, or not at all: four times costs registers)
+#pragma unroll (kColScale ? 1 : 2)
         for (int j = 0; j < 4; ++j, ++q) {
           if (kb4 + j >= n_k) break;
           const int b = q % kBufs;
-          const float s = sj[j];
+          const float s = j == 0 ? sj[0] : j == 1 ? sj[1] : j == 2 ? sj[2] : sj[3];
           const float* cs = S.cs[kColScale ? slot : 0][j] + (kColScale ? half * kCols : 0);
           ok &= f8_wait(&S.acc_full[b], (q / kBufs) & 1u, &S.abort, limit);
           tc::fence_after_sync();
