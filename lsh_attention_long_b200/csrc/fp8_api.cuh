@@ -101,6 +101,15 @@ lsh_status quant_launch(const lsh::QuantArgs& a, int block_rows, cudaStream_t st
                     dim3((unsigned)grid), dim3(256), 0, st, a);
 }
 
+// Two matrices in 1 x 128 blocks (both ways, or transposed alone), one launch.
+lsh_status quant_two_launch(const lsh::QuantArgs& a, const lsh::QuantArgs& b, cudaStream_t st) {
+  const long long na = ((a.rows + 127) / 128) * (long long)kblocks(a.cols);
+  const long long nb = ((b.rows + 127) / 128) * (long long)kblocks(b.cols);
+  if (na + nb > 0x7fffffffLL) return LSH_ERR_UNSUPPORTED;
+  return launch_pdl(lsh::quant_two_kernel, dim3((unsigned)(na + nb)), dim3(256), 0, st, a, b,
+                    (unsigned)na);
+}
+
 lsh::QuantArgs quant_args(int32_t rows, int32_t cols, const void* X, void* Y, float* scales,
                           void* Yt, float* scales_t) {
   lsh::QuantArgs a = {};
@@ -196,15 +205,16 @@ bool fp8_pair_tiles(const lsh::Fp8GemmArgs& g) {
   return 4LL * ceil_div(g.M, 256) * ceil_div(g.N, 256) >= num_sms();
 }
 
-// CTAs that share a 128 x 128 tile's K: as many (up to 8) as leave each two
-// blocks of K and all of them an SM at the same time (clusters of 4 and 8 fit
-// on 132 and 120 SMs).
+// CTAs that share a 128 x 128 tile's K, as many as all get an SM at the same
+// time (15 clusters of 8 or 33 of 4 fit on a B200).  Meeting at the end costs
+// some 2 us, so K has to be long: 64 x 4096 x 4096 takes 9.6 us with four and
+// 13.1 with one, 64 x 2048 x 1024 6.0 and 5.2, 1000 x 512 x 2048 8.1 and 7.5.
 int fp8_split(const lsh::Fp8GemmArgs& g) {
   const long long tiles = (long long)ceil_div(g.M, 128) * ceil_div(g.N, 128);
   const int k = ceil_div(g.K, 128);
-  if (tiles * 8 <= 120 && k >= 16) return 8;
-  if (tiles * 4 <= 132 && k >= 8) return 4;
-  if (tiles * 2 <= num_sms() && k >= 4) return 2;
+  if (tiles <= 15 && k >= 16) return 8;
+  if (tiles <= 33 && k >= 24) return 4;
+  if (tiles * 2 <= num_sms() && k >= 32) return 2;
   return 1;
 }
 
@@ -218,10 +228,19 @@ lsh_status fp8_tc_gemm(const lsh::Fp8TcArgs& a, cudaStream_t st) {
   return fp8_tc_launch<1, 128, lsh::kF8Store, kColScale, 1>(a, st);
 }
 
+// Whether the kernel for few rows is the faster one.  Its MMAs take 8 rows at a
+// time, so from 9 on it needs twice as many and falls behind where they, not
+// the trip to memory, are the larger part: 16 x 2048 x 512 takes 3.6 us with it
+// and 4.0 with tcgen05 tiles, 16 x 4096 x 4096 14.4 and 10.3 (8 rows: 7.3 and
+// 10.3).
+bool fp8_few_rows(const lsh::Fp8GemmArgs& g) {
+  return g.M <= 8 || (g.M <= lsh::kSkMaxM && g.K <= 1024 && g.N <= 8192);
+}
+
 // early_b: see Fp8SkinnyArgs.
 lsh_status fp8_gemm_launch(const lsh::Fp8GemmArgs& g, cudaStream_t st, int order = lsh::kF8Wait,
                            int early_b = 0) {
-  if (g.M <= lsh::kSkMaxM)
+  if (fp8_few_rows(g))
     return fp8_skinny_launch<lsh::kF8Store>(g, nullptr, nullptr, early_b, st);
   lsh::Fp8TcArgs a = {};
   a.g = g;
@@ -233,7 +252,7 @@ lsh_status fp8_gemm_launch(const lsh::Fp8GemmArgs& g, cudaStream_t st, int order
 // The hidden activation of the feed-forward: max(0, A B^T + bias) in 8 bits.
 lsh_status fp8_gemm_quant_launch(const lsh::Fp8GemmArgs& g, void* Q, float* qs, int order,
                                  cudaStream_t st) {
-  if (g.M <= lsh::kSkMaxM) return fp8_skinny_launch<lsh::kF8Quant>(g, Q, qs, 0, st);
+  if (fp8_few_rows(g)) return fp8_skinny_launch<lsh::kF8Quant>(g, Q, qs, 0, st);
   lsh::Fp8TcArgs a = {};
   a.g = g;
   a.Q = static_cast<uint8_t*>(Q);
@@ -436,7 +455,12 @@ lsh_status lsh_matmul_fp8_backward(int32_t M, int32_t N, int32_t K, const void* 
   lsh::QuantArgs q = quant_args(M, N, dC, dA ? w + l.dc : nullptr, f(l.dc_s),
                                 dB ? w + l.dct : nullptr, f(l.dct_s));
   q.colsum = db ? f(l.sums) : nullptr;
-  if ((s = quant_launch<__nv_bfloat16>(q, 1, st)) != LSH_OK) return s;
+  // only what is asked for is put into 8 bits; db alone still reads dC once
+  if (dB)
+    s = quant_two_launch(q, quant_args(M, K, A, nullptr, nullptr, w + l.at, f(l.at_s)), st);
+  else
+    s = quant_launch<__nv_bfloat16>(q, 1, st);
+  if (s != LSH_OK) return s;
   if (db && (s = column_sum(f(l.sums), (int)kblocks(M), N, db, st)) != LSH_OK) return s;
   if (dA) {
     lsh::Fp8GemmArgs g = fp8_gemm_args(M, K, N, w + l.dc, f(l.dc_s), Bt, bt_scales, 128);
@@ -445,8 +469,6 @@ lsh_status lsh_matmul_fp8_backward(int32_t M, int32_t N, int32_t K, const void* 
     if ((s = fp8_gemm_launch(g, st)) != LSH_OK) return s;
   }
   if (dB) {
-    const lsh::QuantArgs qa = quant_args(M, K, A, nullptr, nullptr, w + l.at, f(l.at_s));
-    if ((s = quant_launch<__nv_bfloat16>(qa, 1, st)) != LSH_OK) return s;
     lsh::Fp8GemmArgs g = fp8_gemm_args(N, K, (int)pitch16(M), w + l.dct, f(l.dct_s), w + l.at,
                                        f(l.at_s), 1);
     g.C = dB;

@@ -134,7 +134,7 @@ struct QuantPiece<float> {
 // divisions of a block (its scale and the scale's inverse) are one lane's,
 // which hands the inverse on, and bf16 entries stay packed.
 template <typename XT, bool kSquare>
-__global__ void __launch_bounds__(256, sizeof(XT) == 2 ? 4 : 2) quant_tile_kernel(QuantArgs a) {
+__device__ __forceinline__ void quant_tile(const QuantArgs& a, unsigned block) {
   constexpr bool kBf16 = sizeof(XT) == 2;
   using Piece = QuantPiece<XT>;
   constexpr int kMags = Piece::kMags, kPerMag = 8 / kMags;
@@ -145,8 +145,8 @@ __global__ void __launch_bounds__(256, sizeof(XT) == 2 ? 4 : 2) quant_tile_kerne
   grid_dep_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, rg = tid >> 4, cg = tid & 15;
   const int cb = (a.cols + 127) >> 7;
-  const long long tr = blockIdx.x / cb;  // row block
-  const int tc = (int)(blockIdx.x % cb); // column block
+  const long long tr = block / cb;   // row block
+  const int tc = (int)(block % cb);  // column block
   const long long row0 = tr * 128 + 8 * rg;
   const int col0 = tc * 128 + 8 * cg;
   Piece v[8];
@@ -264,6 +264,19 @@ __global__ void __launch_bounds__(256, sizeof(XT) == 2 ? 4 : 2) quant_tile_kerne
       *reinterpret_cast<uint4*>(a.yt + (size_t)(tc * 128 + c) * a.pitch_t + r) =
           *reinterpret_cast<const uint4*>(tile + c * 128 + (((tid & 7) ^ ((c >> 3) & 7)) << 4));
   }
+}
+
+template <typename XT, bool kSquare>
+__global__ void __launch_bounds__(256, sizeof(XT) == 2 ? 4 : 2) quant_tile_kernel(QuantArgs a) {
+  quant_tile<XT, kSquare>(a, blockIdx.x);
+}
+
+// The tiles of two bf16 matrices, `na` of the first.
+__global__ void __launch_bounds__(256, 4) quant_two_kernel(QuantArgs a, QuantArgs b, unsigned na) {
+  if (blockIdx.x < na)
+    quant_tile<__nv_bfloat16, false>(a, blockIdx.x);
+  else
+    quant_tile<__nv_bfloat16, false>(b, blockIdx.x - na);
 }
 
 }  // namespace lsh

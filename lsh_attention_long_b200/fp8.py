@@ -126,11 +126,11 @@ def lsh_rmsnorm_forward(X, w, *, R=None, eps: float = 1e-6, out_dtype=None, H=No
         if R is not None and H is None:
             H = torch.empty_like(X)
         if Y is None:
-            Y = torch.empty(shape, dtype=yt, device=dev)
+            Y = torch.empty_like(X, dtype=yt)
         if yt is F8 and scales is None:
-            scales = torch.empty((rows, _up(cols, 128) // 128), dtype=f32, device=dev)
+            scales = X.new_empty((rows, _up(cols, 128) // 128), dtype=f32)
         if rstd is None and want_rstd:
-            rstd = torch.empty((rows,), dtype=f32, device=dev)
+            rstd = X.new_empty((rows,), dtype=f32)
         _go("lsh_rmsnorm_forward", dev, rows, cols, _CODES[X.dtype], _CODES[rt], _CODES[w.dtype],
             _CODES[yt], X.data_ptr(), _p(R), w.data_ptr(), eps, _p(H), Y.data_ptr(), _p(scales),
             _p(rstd))
@@ -155,7 +155,7 @@ def lsh_rmsnorm_backward(dY, H, w, rstd, *, dH=None, dX=None, dw=None, ws=None, 
         if dX is None:
             dX = torch.empty_like(H)
         if dw is None:
-            dw = torch.empty((cols,), dtype=f32, device=dev)
+            dw = H.new_empty((cols,), dtype=f32)
         ws, wp, wn = _scratch("lsh_rmsnorm_bwd_ws_size", (rows, cols), ws, dev)
         _go("lsh_rmsnorm_backward", dev, rows, cols, _CODES[H.dtype], _CODES[dY.dtype],
             _CODES[w.dtype], dY.data_ptr(), H.data_ptr(), w.data_ptr(), rstd.data_ptr(), _p(dH),
@@ -182,14 +182,14 @@ def lsh_quantize_fp8(X, *, block_rows: int = 1, transposed: bool = False, Y=None
                   ("scales_t", scales_t, t_shape, f32))
     with _on(dev, stream):
         if Y is None:
-            Y = torch.empty((rows, cols), dtype=F8, device=dev)
+            Y = torch.empty_like(X, dtype=F8)
         if scales is None:
-            scales = torch.empty(s_shape, dtype=f32, device=dev)
+            scales = X.new_empty(s_shape, dtype=f32)
         if transposed:
             if Yt is None:
-                Yt = torch.empty(yt_shape, dtype=F8, device=dev)
+                Yt = X.new_empty(yt_shape, dtype=F8)
             if scales_t is None:
-                scales_t = torch.empty(t_shape, dtype=f32, device=dev)
+                scales_t = X.new_empty(t_shape, dtype=f32)
         _go("lsh_quantize_fp8", dev, rows, cols, _CODES[X.dtype], br, X.data_ptr(), Y.data_ptr(),
             scales.data_ptr(), _p(Yt), _p(scales_t))
     return (Y, scales, Yt, scales_t) if transposed else (Y, scales)
@@ -212,7 +212,7 @@ def lsh_matmul_fp8(A, a_scales, B, b_scales, *, bias=None, relu: bool = False,
                   ("bias", bias, (N,), torch.bfloat16), ("C", C, (M, N), out_dtype))
     with _on(dev, stream):
         if C is None:
-            C = torch.empty((M, N), dtype=out_dtype, device=dev)
+            C = A.new_empty((M, N), dtype=out_dtype)
         ws, wp, wn = _scratch("lsh_matmul_fp8_ws_size", (M, N, K), ws, dev)
         _go("lsh_matmul_fp8", dev, M, N, K, A.data_ptr(), a_scales.data_ptr(), B.data_ptr(),
             b_scales.data_ptr(), 1 if rowwise else 128, _p(bias), int(relu), _CODES[out_dtype],
@@ -235,11 +235,11 @@ def lsh_matmul_fp8_backward(dC, A, Bt, bt_scales, *, out_dtype=torch.bfloat16, d
                   ("dA", dA, (M, K), out_dtype), ("dB", dB, (N, K), f32), ("db", db, (N,), f32))
     with _on(dev, stream):
         if dA is None:
-            dA = torch.empty((M, K), dtype=out_dtype, device=dev)
+            dA = torch.empty_like(A, dtype=out_dtype)
         if dB is None:
-            dB = torch.empty((N, K), dtype=f32, device=dev)
+            dB = A.new_empty((N, K), dtype=f32)
         if db is None:
-            db = torch.empty((N,), dtype=f32, device=dev)
+            db = A.new_empty((N,), dtype=f32)
         ws, wp, wn = _scratch("lsh_matmul_fp8_bwd_ws_size", (M, N, K), ws, dev)
         _go("lsh_matmul_fp8_backward", dev, M, N, K, dC.data_ptr(), A.data_ptr(), Bt.data_ptr(),
             bt_scales.data_ptr(), _CODES[out_dtype], dA.data_ptr(), dB.data_ptr(), db.data_ptr(),
@@ -271,7 +271,7 @@ def lsh_ffn_forward_fp8(X, x_scales, W1, w1_scales, b1, W2, w2_scales, b2, chunk
                   ("Y", Y, X.shape, bf))
     with _on(dev, stream):
         if Y is None:
-            Y = torch.empty(X.shape, dtype=bf, device=dev)
+            Y = torch.empty_like(X, dtype=bf)
         ws, wp, wn = _scratch("lsh_ffn_fp8_ws_size", (tokens, d_model, d_ff, chunk), ws, dev)
         _go("lsh_ffn_forward_fp8", dev, tokens, d_model, d_ff, chunk, X.data_ptr(),
             x_scales.data_ptr(), W1.data_ptr(), w1_scales.data_ptr(), b1.data_ptr(),
