@@ -28,19 +28,35 @@ __device__ __forceinline__ float block_amax(uint32_t bits) {
   return __uint_as_float(bits > lo ? bits : lo);
 }
 
-// 448 v / m from inv = 448 / m (rounded): within 2^-22 of the quotient.  For
-// v and m of 8 significant bits (bf16) the quotient is either one of the
-// 5-bit numbers where e4m3 codes border on each other or at least 2^-13 away
-// from all of them: 448 v / m = 7 a / b with integers a, b < 256 up to a
-// power of two, a border is c < 32 up to one, and |7 a 2^u - c b| >= 1 unless
-// equal, so the relative distance is at least 1 / (31 * 255).  Rounding the
-// product to 16 significant bits first (error 2^-17) therefore puts the
-// former exactly on the border, where ties go to even as the definition asks,
-// and leaves the latter on their side.
+// The quotient 448 v / m of an entry, from inv = 448 / m (rounded): v * inv is
+// within 2^-22 of it, which would put one entry in some 10^5 on the wrong side
+// of the border between two codes, and bf16 entries far more often, since their
+// quotients often are borders.
+//
+// v and m of 8 significant bits (bf16): the quotient is either one of the 5-bit
+// numbers where e4m3 codes border on each other or at least 2^-13 away from all
+// of them: 448 v / m = 7 a / b with integers a, b < 256 up to a power of two, a
+// border is c < 32 up to one, and |7 a 2^u - c b| >= 1 unless equal, so the
+// relative distance is at least 1 / (31 * 255).  Rounding the product to 16
+// significant bits first (error 2^-17) therefore puts the former exactly on the
+// border, where ties go to even as the definition asks, and leaves the latter
+// on their side.
+//
+// fp32: one step of Newton's method on q m' = 0.875 v, m' = m / 512, whose
+// remainder is exact but for the last bits (0.875 v as a sum of two floats, the
+// product inside an fma), gives the quotient to its last bit or so.
+struct BlockScale {
+  float inv, amax;
+  __device__ __forceinline__ explicit BlockScale(float am) : inv(kE4m3Max / am), amax(am) {}
+  __device__ __forceinline__ BlockScale(float i, float am) : inv(i), amax(am) {}
+};
 template <bool kFromBf16>
-__device__ __forceinline__ float scale_to_e4m3(float v, float inv) {
-  const float p = v * inv;
-  return kFromBf16 ? __uint_as_float((__float_as_uint(p) + 0x80u) & 0xffffff00u) : p;
+__device__ __forceinline__ float scale_to_e4m3(float v, const BlockScale& b) {
+  const float q = v * b.inv;
+  if (kFromBf16) return __uint_as_float((__float_as_uint(q) + 0x80u) & 0xffffff00u);
+  const float hi = 0.875f * v, lo = fmaf(0.875f, v, -hi);
+  const float left = fmaf(-q, b.amax * (1.f / 512.f), hi) + lo;
+  return fmaf(left, b.inv * (512.f / 448.f), q);
 }
 
 // Two or four codes, the first in the lowest byte.

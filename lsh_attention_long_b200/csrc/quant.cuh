@@ -49,9 +49,10 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(QuantArgs a) {
 #pragma unroll
   for (int o = 8; o; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
   if (!in) return;
-  const float am = block_amax(m), inv = kE4m3Max / am;
+  const float am = block_amax(m);
+  const BlockScale sc(am);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = scale_to_e4m3<kBf16>(v[e], inv);
+  for (int e = 0; e < 8; ++e) v[e] = scale_to_e4m3<kBf16>(v[e], sc);
   *reinterpret_cast<uint2*>(a.y + at) =
       make_uint2(e4m3x4(v[0], v[1], v[2], v[3]), e4m3x4(v[4], v[5], v[6], v[7]));
   if ((p & 15) == 0) a.scales[(size_t)row * (padded >> 4) + (p >> 4)] = am / kE4m3Max;
@@ -140,7 +141,7 @@ __device__ __forceinline__ void quant_tile(const QuantArgs& a, unsigned block) {
   constexpr int kMags = Piece::kMags, kPerMag = 8 / kMags;
   __shared__ uint32_t cmax[8][128 / kPerMag];
   __shared__ float csum[8][128];
-  __shared__ float cinv[128];
+  __shared__ float cinv[128], cam[128];
   __shared__ __align__(16) uint8_t tile[128 * 128];
   grid_dep_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, rg = tid >> 4, cg = tid & 15;
@@ -158,7 +159,7 @@ __device__ __forceinline__ void quant_tile(const QuantArgs& a, unsigned block) {
       v[i].zero();
   }
   grid_dep_launch();
-  float inv_sq = 0.f;
+  BlockScale sq(0.f, 0.f);
   if (kSquare) {  // one maximum for the whole tile
     uint32_t m = 0;
 #pragma unroll
@@ -170,7 +171,7 @@ __device__ __forceinline__ void quant_tile(const QuantArgs& a, unsigned block) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) m = max(m, cmax[i][0]);
     const float am = block_amax(m);
-    inv_sq = kE4m3Max / am;
+    sq = BlockScale(am);
     if (tid == 0) {
       const long long rb = (a.rows + 127) >> 7;
       if (a.y) a.scales[tr * cb + tc] = am / kE4m3Max;
@@ -178,23 +179,27 @@ __device__ __forceinline__ void quant_tile(const QuantArgs& a, unsigned block) {
     }
   }
   if (a.y) {
-    float inv_row = 0.f;  // of row (cg & 14) / 2
+    BlockScale mine(0.f, 0.f);  // of row (cg & 14) / 2
     if (!kSquare) {
       uint32_t m[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) m[i] = v[i].amax();
       const float am = block_amax(rows_amax(m, lane));
-      inv_row = kE4m3Max / am;
+      mine = BlockScale(am);
       const long long r = row0 + (cg >> 1);
       if (!(cg & 1) && r < a.rows) a.scales[(size_t)r * cb + tc] = am / kE4m3Max;
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float inv =
-          kSquare ? inv_sq : __shfl_sync(0xffffffffu, inv_row, (lane & 16) + 2 * i);
+      BlockScale sc = sq;
+      if (!kSquare) {
+        const int from = (lane & 16) + 2 * i;
+        sc.inv = __shfl_sync(0xffffffffu, mine.inv, from);
+        if (!kBf16) sc.amax = __shfl_sync(0xffffffffu, mine.amax, from);
+      }
       float q[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) q[e] = scale_to_e4m3<kBf16>(v[i].get(e), inv);
+      for (int e = 0; e < 8; ++e) q[e] = scale_to_e4m3<kBf16>(v[i].get(e), sc);
       if (row0 + i < a.rows && col0 < a.cols)
         *reinterpret_cast<uint2*>(a.y + (size_t)(row0 + i) * a.cols + col0) =
             make_uint2(e4m3x4(q[0], q[1], q[2], q[3]), e4m3x4(q[4], q[5], q[6], q[7]));
@@ -230,6 +235,7 @@ __device__ __forceinline__ void quant_tile(const QuantArgs& a, unsigned block) {
         for (int i = 1; i < 8; ++i) m = Piece::max2(m, cmax[i][tid / kPerMag]);
         const float am = block_amax(Piece::column(m, tid));
         cinv[tid] = kE4m3Max / am;
+        cam[tid] = am;
         if (c < a.cols) a.scales_t[(size_t)c * ((a.rows + 127) >> 7) + tr] = am / kE4m3Max;
       }
     } else if (a.colsum && c < a.cols) {
@@ -246,10 +252,10 @@ __device__ __forceinline__ void quant_tile(const QuantArgs& a, unsigned block) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     const int c = 8 * cg + e;
-    const float inv = kSquare ? inv_sq : cinv[c];
+    const BlockScale sc = kSquare ? sq : BlockScale(cinv[c], cam[c]);
     float q[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = scale_to_e4m3<kBf16>(v[i].get(e), inv);
+    for (int i = 0; i < 8; ++i) q[i] = scale_to_e4m3<kBf16>(v[i].get(e), sc);
     *reinterpret_cast<uint2*>(tile + c * 128 + ((((rg >> 1) ^ (cg & 7)) << 4) | ((rg & 1) << 3))) =
         make_uint2(e4m3x4(q[0], q[1], q[2], q[3]), e4m3x4(q[4], q[5], q[6], q[7]));
   }
