@@ -257,7 +257,8 @@ def lsh_ffn_forward_fp8(X, x_scales, W1, w1_scales, b1, W2, w2_scales, b2, chunk
                         ws=None, stream=None):
     """Chunked feed-forward in 8 bits: Y = W2 q(max(0, W1 x + b1)) + b2 (bf16) per position of X
     [..., d_model] (1 x 128 blocks, x_scales [tokens, ceil(d_model / 128)]; W1 [d_ff, d_model] and
-    W2 [d_model, d_ff] in 128 x 128 blocks), `chunk` positions at a time."""
+    W2 [d_model, d_ff] in 128 x 128 blocks), `chunk` positions at a time, or as many as have a
+    hidden activation of 32 MB."""
     if not isinstance(X, torch.Tensor) or X.dim() < 2:
         raise ValueError("X must be a [..., d_model] tensor")
     d_model, bf, f32 = X.shape[-1], torch.bfloat16, torch.float32

@@ -258,7 +258,10 @@ def sum_tol(K):
 PRODUCTS = [(1, 16, 16), (1, 144, 272), (3, 512, 2048), (8, 4096, 128), (9, 256, 512), (16, 640, 1024),
             (17, 128, 400), (33, 2064, 144), (64, 512, 512), (100, 272, 656), (128, 256, 128),
             (129, 272, 1040), (200, 1024, 4096), (256, 512, 384), (1000, 656, 400),
-            (2049, 528, 208)]
+            (2049, 528, 208),
+            # pairs of CTAs on 256 x 256 tiles; K shared by 8, 4 and 2 CTAs; few rows, long K
+            (2500, 1040, 400), (8200, 272, 128), (300, 640, 2064), (64, 4096, 3088),
+            (256, 4096, 4112), (12, 512, 1040), (16, 272, 4096)]
 
 
 @pytest.mark.parametrize("M,N,K", PRODUCTS)
@@ -348,7 +351,8 @@ def ffn(s, chunk, **kw):
 @pytest.mark.parametrize("T,D,F,chunk", [(1, 16, 16, 128), (1, 512, 2048, 128), (4, 512, 2048, 128),
                                          (16, 272, 1040, 128), (17, 128, 400, 128),
                                          (129, 256, 512, 128), (300, 144, 656, 256),
-                                         (1000, 512, 2048, 384), (2048, 768, 1024, 8192)])
+                                         (1000, 512, 2048, 384), (2048, 768, 1024, 8192),
+                                         (2500, 272, 1040, 8192), (12, 1040, 272, 128)])
 def test_ffn(T, D, F, chunk):
     s = ffn_state(T, D, F)
     Y, intact = guarded((T, D), BF)
@@ -376,12 +380,27 @@ def test_ffn(T, D, F, chunk):
     close(Y, want, tol + HALF[BF] * (want.abs() + tol), "Y")
 
 
-def test_ffn_chunks_do_not_change_the_result():
-    s = ffn_state(1000, 256, 512)
-    Y = ffn(s, 1024)
-    for chunk in (128, 384):
-        assert torch.equal(Y, ffn(s, chunk))
+@pytest.mark.parametrize("T,D,F,chunk", [(9000, 64, 8208, 128), (20000, 128, 4112, 4096)])
+def test_ffn_of_several_chunks(T, D, F, chunk):
+    """Enough positions for three chunks and more, whose products overlap from launch to launch and
+    take turns on two buffers: the same as each position's own row of one call on it alone, up to
+    the order of fp32 sums, and the same bits on every run."""
+    s = ffn_state(T, D, F)
+    ws = L.ffn_fp8_workspace(T, D, F, chunk, torch.device("cuda"))
+    assert ws.numel() < 2.2 * (max(32 << 20, chunk * F) + (1 << 20)) < T * F * 2
+    ws.fill_(0x7f)  # NaN wherever something is read before it is written
+    first = ffn(s, chunk, ws=ws).clone()
     ok()
+    assert not first.isnan().any()
+    for _ in range(10):
+        assert torch.equal(ffn(s, chunk, ws=ws), first)
+    ok()
+    rows = torch.arange(0, T, 97, device="cuda")
+    part = dict(s, X8=s["X8"].view(torch.uint8)[rows].view(F8), sx=s["sx"][rows])
+    alone = ffn(part, chunk).double()
+    # a sum in another order may put a hidden entry on the next code: 2^-4 of it, one in
+    # thousands; the outputs are of order one
+    close(first[rows].double(), alone, 2 * HALF[BF] * alone.abs() + 2.0 ** -6, "rows alone")
 
 
 # ------------------------------------------------------------------ together
