@@ -412,8 +412,9 @@ LSH_API lsh_status lsh_ffn_forward_fp8(int32_t tokens, int32_t d_model, int32_t 
  * limit of clock cycles (about 2 s by default), records LSH_ERR_TIMEOUT in
  * the device status word, stops its thread block cleanly (in-flight copies and
  * tensor-core operations finish, tensor memory is freed) and returns.
- *   wait_cycles > 0   the limit of the waits of the tensor-core attention and
- *                     feed-forward kernels for the calls that follow; 0
+ *   wait_cycles > 0   the limit of the waits of the tensor-core attention,
+ *                     feed-forward and 8-bit product kernels for the calls that
+ *                     follow (not of the waits for what is in flight); 0
  *                     restores the default;
  *   hold_tile >= 0    in the calls that follow, the tensor-core attention
  *                     kernel's producers stop before tile `hold_tile` of each

@@ -232,24 +232,19 @@ __global__ void __launch_bounds__(kF8Threads, 1)
           }
         }
       }
-      // every load issued has landed before the block leaves: the even rank
+      // Every load issued has landed before the block leaves: the even rank
       // (which leaves together with the odd one) waits for the last stages.
-      // After an abort it may have fewer to wait for than the odd rank has in
-      // flight, which then gives them time (far more than a load takes).
+      // After an abort one rank may have issued loads that the other's barrier
+      // does not expect; then both give them time, far more than a load takes.
       if (kPair == 2 && *(volatile int*)&S.abort) {
         const long long t0 = clock64();
         while (clock64() - t0 < 2000000) {
         }
-      }
-      const uint32_t first = rank ? q : q > (uint32_t)kStages ? q - kStages : 0;
-      for (uint32_t p = first; p < q; ++p) {
-        const long long t0 = clock64();
-        while (!tc::mbar_test(&S.full[p % kStages], (p / kStages) & 1u)) {
-          if (clock64() - t0 > limit) {
+      } else {
+        const uint32_t first = rank ? q : q > (uint32_t)kStages ? q - kStages : 0;
+        for (uint32_t p = first; p < q; ++p)
+          if (!tc::mbar_wait(&S.full[p % kStages], (p / kStages) & 1u))
             record_status(tc::kErrTimeout);
-            break;
-          }
-        }
       }
     }
     __syncwarp();
@@ -286,13 +281,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
       // every MMA issued has finished before tensor memory is freed
       if (tc::elect_one()) {
         commit(&S.mma_done[warp - 1]);
-        const long long t0 = clock64();
-        while (!tc::mbar_test(&S.mma_done[warp - 1], 0)) {
-          if (clock64() - t0 > limit) {
-            record_status(tc::kErrTimeout);
-            break;
-          }
-        }
+        if (!tc::mbar_wait(&S.mma_done[warp - 1], 0)) record_status(tc::kErrTimeout);
       }
     }
     __syncwarp();

@@ -506,3 +506,50 @@ def test_repeated_calls_give_the_same_bits():
         first = first or out
         assert all(torch.equal(a, b) for a, b in zip(first, out))
     ok()
+
+
+# ------------------------------------------------------------------ failure path, parts of calls
+
+@pytest.mark.parametrize("M,N,K,b_rows", [(128, 256, 1040, 128),    # one CTA to a tile
+                                          (300, 640, 2064, 1),      # a cluster sharing K
+                                          (2500, 1040, 400, 128),   # a pair
+                                          (2500, 1040, 400, 1)])
+def test_product_waits_that_run_out_are_reported_and_recovered(M, N, K, b_rows):
+    """With a limit of one cycle a wait that is not over at its first look gives up: the call reports
+    it, unless none had to wait, and the next one is as before."""
+    g = gen(M)
+    A, sa = codes(g, M, K, 1)
+    B, sb = codes(g, N, K, b_rows)
+    want = L.lsh_matmul_fp8(A, sa, B, sb)
+    ok()
+    L.lsh_set_wait_test(-1, 1)
+    try:
+        got = L.lsh_matmul_fp8(A, sa, B, sb)
+        status = L.lsh_device_status()
+    finally:
+        L.lsh_set_wait_test(-1, 0)
+    assert status == 5 or (status == 0 and torch.equal(got, want))  # LSH_ERR_TIMEOUT
+    assert torch.equal(L.lsh_matmul_fp8(A, sa, B, sb), want)
+    ok()
+
+
+def test_gradients_asked_for_one_by_one():
+    """The library's own entry point leaves out what its caller does not ask for."""
+    import ctypes
+    lib = L.load_library()
+    g = gen(11)
+    M, N, K = 200, 144, 272
+    dC, A = rnd(g, M, N, t=BF), rnd(g, M, K, t=BF)
+    _, _, Bt, st = L.lsh_quantize_fp8(rnd(g, N, K), block_rows=128, transposed=True)
+    want = L.lsh_matmul_fp8_backward(dC, A, Bt, st, out_dtype=F32)
+    n = lib.lsh_matmul_fp8_bwd_ws_size(M, N, K)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    for which in (0, 1, 2):
+        out = torch.full_like(want[which], float("nan"))
+        p = [out.data_ptr() if i == which else None for i in range(3)]
+        rc = lib.lsh_matmul_fp8_backward(
+            M, N, K, dC.data_ptr(), A.data_ptr() if which == 1 else None,
+            Bt.data_ptr() if which == 0 else None, st.data_ptr() if which == 0 else None, 0, *p,
+            ws.data_ptr(), n, ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+        ok()
+        assert rc == 0 and torch.equal(out, want[which])
