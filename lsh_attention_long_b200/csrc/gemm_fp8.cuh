@@ -29,4 +29,14 @@ __device__ __forceinline__ float relu_nan(float v) {
   return r;
 }
 
+// The codes of max(0, v[0 .. 3] * scale).
+__device__ __forceinline__ uint32_t e4m3x4_relu(const float* v, float scale) {
+  const float2 a = __fmul2_rn(make_float2(v[0], v[1]), make_float2(scale, scale));
+  const float2 b = __fmul2_rn(make_float2(v[2], v[3]), make_float2(scale, scale));
+  uint16_t lo, hi;
+  asm("cvt.rn.satfinite.relu.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(a.y), "f"(a.x));
+  asm("cvt.rn.satfinite.relu.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(b.y), "f"(b.x));
+  return (uint32_t)lo | ((uint32_t)hi << 16);
+}
+
 }  // namespace lsh

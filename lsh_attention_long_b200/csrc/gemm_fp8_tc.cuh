@@ -377,9 +377,21 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     bool ok = true;
     for (int u = first_unit; u < n_units; u += unit_step, ++tile) {
       const int m0 = (u / n_n * kPair + rank) * kF8BM, c0 = (u % n_n) * kBN + half * kCols;
+      // the totals start from the bias, which comes with the tile's first scales
+      // (with kSplit it is added at the end, once)
       float acc[kCols];
+      if (!kSplit && g.bias) {
+        ok &= f8_wait(&S.sc_full[qs % kF8Slots], (qs / kF8Slots) & 1u, &S.abort, limit);
+        const float4* bias = S.bias[tile % 4] + half * (kCols / 4);
 #pragma unroll
-      for (int e = 0; e < kCols; ++e) acc[e] = 0.f;
+        for (int e = 0; e < kCols; e += 4) {
+          const float4 t = bias[e / 4];
+          acc[e] = t.x; acc[e + 1] = t.y; acc[e + 2] = t.z; acc[e + 3] = t.w;
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < kCols; ++e) acc[e] = 0.f;
+      }
       for (int kb4 = 0; kb4 < n_k; kb4 += 4, ++qs) {
         const int slot = qs % kF8Slots;
         // after an abort every wait returns at once; the loop runs on to its
@@ -441,7 +453,10 @@ __global__ void __launch_bounds__(kF8Threads, 1)
         grid_dep_wait();
         grid_dep_launch();
       }
-      const bool bad = f8_any(!ok);  // for all of them, or none
+      // where the warps share barriers below, they all go on or none does
+      const bool bad = kSplit || (kEpi == kF8Quant && kCols == 64)
+                           ? f8_any(!ok)
+                           : !__all_sync(0xffffffffu, ok);
       if (bad && !kSplit) break;
       if (kSplit) {
         // Each CTA of the cluster adds up kCols / kParts columns of every
@@ -507,15 +522,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
         }
         __syncwarp();
       };
-      if (g.bias) {
-        const float4* bias = S.bias[tile % 4] + half * (kCols / 4);
-#pragma unroll
-        for (int e = 0; e < kCols; e += 4) {
-          const float4 t = bias[e / 4];
-          acc[e] += t.x; acc[e + 1] += t.y; acc[e + 2] += t.z; acc[e + 3] += t.w;
-        }
-      }
-      if (kEpi == kF8Quant || g.relu) {
+      if (kEpi == kF8Store && g.relu) {
 #pragma unroll
         for (int e = 0; e < kCols; ++e) acc[e] = relu_nan(acc[e]);
       }
@@ -524,9 +531,13 @@ __global__ void __launch_bounds__(kF8Threads, 1)
         // rest of their block)
         // a block is the thread's 128 columns, or (kBN = 128) its 64 and those
         // of the other warpgroup's thread of the same row
-        uint32_t m = 0;
+        // max(0, .) costs nothing here: as signed integers the positive numbers
+        // compare like numbers and the negative ones are below zero (a NaN that
+        // arithmetic made is the largest), and the conversion has it built in
+        int mi = 0;
 #pragma unroll
-        for (int e = 0; e < kCols; ++e) m = max(m, __float_as_uint(acc[e]));  // none is negative
+        for (int e = 0; e < kCols; ++e) mi = max(mi, __float_as_int(acc[e]));
+        uint32_t m = (uint32_t)mi;
         if (kCols == 64) {
           S.amax[half][et] = m;
           asm volatile("bar.sync 1, 256;" ::: "memory");
@@ -540,11 +551,8 @@ __global__ void __launch_bounds__(kF8Threads, 1)
 #pragma unroll
         for (int p = 0; p < kCols / 16; ++p) {
           const float* v = acc + 16 * p;
-          const uint4 w = make_uint4(
-              e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
-              e4m3x4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv),
-              e4m3x4(v[8] * inv, v[9] * inv, v[10] * inv, v[11] * inv),
-              e4m3x4(v[12] * inv, v[13] * inv, v[14] * inv, v[15] * inv));
+          const uint4 w = make_uint4(e4m3x4_relu(v, inv), e4m3x4_relu(v + 4, inv),
+                                     e4m3x4_relu(v + 8, inv), e4m3x4_relu(v + 12, inv));
           if (kCols == 128)
             *reinterpret_cast<uint4*>(my_row + ((p ^ swz) << 4)) = w;
           else if (m0 + et < g.M && c0 + 16 * p < g.N)  // two whole sectors of the row
