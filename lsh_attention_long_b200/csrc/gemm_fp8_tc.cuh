@@ -42,13 +42,15 @@ namespace lsh {
 
 constexpr int kF8Threads = 384;
 // Registers: 168 a thread at launch (what 384 threads can have).  The first
-// warpgroup gives some up, twice as many warps share them: to each epilogue
-// thread 56 more, or 40 where the scales' warp (which holds a tile's column
-// scales too) needs its own.
+// warpgroup gives some up, which twice as many warps share: most where an
+// epilogue thread has 128 totals, fewer where the scales' warp has a tile's
+// column scales in its own, fewest with 64 totals.
 constexpr int kF8Regs = 168;
-__host__ __device__ constexpr int f8_regs_low(bool col_scale) { return col_scale ? 88 : 56; }
-__host__ __device__ constexpr int f8_regs_high(bool col_scale) {
-  return kF8Regs + (kF8Regs - f8_regs_low(col_scale)) / 2;
+__host__ __device__ constexpr int f8_regs_low(int bn, bool col_scale) {
+  return bn == 128 ? 104 : col_scale ? 88 : 56;
+}
+__host__ __device__ constexpr int f8_regs_high(int bn, bool col_scale) {
+  return kF8Regs + (kF8Regs - f8_regs_low(bn, col_scale)) / 2;
 }
 constexpr int kF8BM = 128, kF8BK = 128;
 
@@ -205,7 +207,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   const int k_lo = kSplit ? part * k_all / kParts : 0;
   const int n_k = kSplit ? (part + 1) * k_all / kParts - k_lo : k_all;
 
-  if (warp < 4) tc::reg_dec<f8_regs_low(kColScale)>();
+  if (warp < 4) tc::reg_dec<f8_regs_low(kBN, kColScale)>();
   if (warp == 0) {
     // ------------------------------------------------------------ TMA loads
     if (lane == 0) {
@@ -290,6 +292,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     // Lane t has rows t, t + 32, .. (and columns t, t + 32, ..); four blocks'
     // scales are in flight at once.
     constexpr int kC = kColScale ? kBN / 32 : 2;
+    const bool vec = k_all % 4 == 0 && k_lo % 4 == 0;
     uint32_t q = 0, tile = 0;
     bool ok = true;
     for (int u = first_unit; u < n_units && ok; u += unit_step, ++tile) {
@@ -308,15 +311,25 @@ __global__ void __launch_bounds__(kF8Threads, 1)
         pb[i] = g.sb + (size_t)((n < g.N ? n : g.N - 1) / (kColScale ? 1 : g.b_rows)) * k_all + k_lo;
       }
       for (int kb = 0; kb < n_k && ok; kb += 4, ++q) {
-        float va[4][4], vb[kC][4];
+        // four blocks' scales of a row: one load where the rows allow it (what
+        // lies past this CTA's blocks is not used), else one each
+        const auto load4 = [&](const float* row) {
+          float4 v;
+          if (vec) {
+            v = *reinterpret_cast<const float4*>(row + kb);
+          } else {
+            v.x = row[kb];
+            v.y = row[kb + 1 < n_k ? kb + 1 : n_k - 1];
+            v.z = row[kb + 2 < n_k ? kb + 2 : n_k - 1];
+            v.w = row[kb + 3 < n_k ? kb + 3 : n_k - 1];
+          }
+          return v;
+        };
+        float4 va[4], vb[kC];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int k = kb + j < n_k ? kb + j : n_k - 1;
+        for (int i = 0; i < 4; ++i) va[i] = load4(pa[i]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) va[i][j] = pa[i][k];
-#pragma unroll
-          for (int i = 0; i < kC; ++i) vb[i][j] = pb[i][k];
-        }
+        for (int i = 0; i < kC; ++i) vb[i] = load4(pb[i]);
         const int slot = q % kF8Slots;
         float4 bias[kBN / 128];
         if (kb == 0 && g.bias) {
@@ -342,19 +355,22 @@ __global__ void __launch_bounds__(kF8Threads, 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           if (kColScale) {
-            S.rs[slot][0][lane + 32 * i] = make_float4(va[i][0], va[i][1], va[i][2], va[i][3]);
+            S.rs[slot][0][lane + 32 * i] = va[i];
           } else {
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-              S.rs[slot][h][lane + 32 * i] = make_float4(va[i][0] * vb[h][0], va[i][1] * vb[h][1],
-                                                      va[i][2] * vb[h][2], va[i][3] * vb[h][3]);
+              S.rs[slot][h][lane + 32 * i] = make_float4(va[i].x * vb[h].x, va[i].y * vb[h].y,
+                                                         va[i].z * vb[h].z, va[i].w * vb[h].w);
           }
         }
         if (kColScale) {
 #pragma unroll
-          for (int i = 0; i < kC; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) S.cs[slot][j][lane + 32 * i] = vb[i][j];
+          for (int i = 0; i < kC; ++i) {
+            S.cs[slot][0][lane + 32 * i] = vb[i].x;
+            S.cs[slot][1][lane + 32 * i] = vb[i].y;
+            S.cs[slot][2][lane + 32 * i] = vb[i].z;
+            S.cs[slot][3][lane + 32 * i] = vb[i].w;
+          }
         }
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&S.sc_full[slot]);
@@ -362,7 +378,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     }
   } else {
     // ------------------------------------------------------------ epilogue
-    tc::reg_inc<f8_regs_high(kColScale)>();
+    tc::reg_inc<f8_regs_high(kBN, kColScale)>();
     const int sub = warp & 3;          // TMEM lanes 32 * sub .. 32 * sub + 31
     const int half = (warp - 4) >> 2;  // which half of the tile's columns
     const int et = (sub << 5) | lane;  // row in the tile
@@ -400,7 +416,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
         const float4 s4 = S.rs[slot][kColScale ? 0 : half][et];
         const float sj[4] = {s4.x, s4.y, s4.z, s4.w};
         // (unrolled twice, or not at all: four times costs registers)
-#pragma unroll (kColScale ? 1 : 2)
+#pragma unroll (kColScale || kBN == 128 ? 1 : 2)
         for (int j = 0; j < 4; ++j, ++q) {
           if (kb4 + j >= n_k) break;
           const int b = q % kBufs;
