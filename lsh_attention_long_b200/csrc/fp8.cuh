@@ -42,21 +42,21 @@ __device__ __forceinline__ float block_amax(uint32_t bits) {
 // border, where ties go to even as the definition asks, and leaves the latter
 // on their side.
 //
-// fp32: one step of Newton's method on q m' = 0.875 v, m' = m / 512, whose
-// remainder is exact but for the last bits (0.875 v as a sum of two floats, the
-// product inside an fma), gives the quotient to its last bit or so.
+// fp32: 448 / m is carried as a sum of two floats, inv + lo, and v * inv as its
+// rounded product and the rest, which an fma gives exactly; their sum is the
+// quotient to half a unit of its last place or hardly more.
 struct BlockScale {
-  float inv, amax;
-  __device__ __forceinline__ explicit BlockScale(float am) : inv(kE4m3Max / am), amax(am) {}
-  __device__ __forceinline__ BlockScale(float i, float am) : inv(i), amax(am) {}
+  float inv, lo;
+  __device__ __forceinline__ explicit BlockScale(float am) : inv(kE4m3Max / am) {
+    lo = fmaf(-inv, am, kE4m3Max) * inv * (1.f / kE4m3Max);
+  }
+  __device__ __forceinline__ BlockScale(float i, float l) : inv(i), lo(l) {}
 };
 template <bool kFromBf16>
 __device__ __forceinline__ float scale_to_e4m3(float v, const BlockScale& b) {
   const float q = v * b.inv;
   if (kFromBf16) return __uint_as_float((__float_as_uint(q) + 0x80u) & 0xffffff00u);
-  const float hi = 0.875f * v, lo = fmaf(0.875f, v, -hi);
-  const float left = fmaf(-q, b.amax * (1.f / 512.f), hi) + lo;
-  return fmaf(left, b.inv * (512.f / 448.f), q);
+  return q + fmaf(v, b.lo, fmaf(v, b.inv, -q));
 }
 
 // Two or four codes, the first in the lowest byte.

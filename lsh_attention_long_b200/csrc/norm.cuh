@@ -103,7 +103,8 @@ struct Raw8 {
 };
 
 template <typename XT, int kOut, int kNV, int kT>
-__global__ void __launch_bounds__(norm_block(kT)) rmsnorm_fwd_kernel(NormArgs a) {
+__global__ void __launch_bounds__(norm_block(kT), kT == 256 && kNV == 1 ? 8 : 1)  // 8: a full SM
+    rmsnorm_fwd_kernel(NormArgs a) {
   __shared__ float red[32];
   grid_dep_wait();
   grid_dep_launch();
@@ -167,11 +168,13 @@ __global__ void __launch_bounds__(norm_block(kT)) rmsnorm_fwd_kernel(NormArgs a)
       for (int e = 0; e < 8; ++e) m = max(m, mag_bits(h[i][e]));
 #pragma unroll
       for (int o = 8; o; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-      const float am = block_amax(m), inv = kE4m3Max / am;
+      const float am = block_amax(m);
+      const BlockScale sc(am);
       if (in) {
-        const uint2 q = make_uint2(
-            e4m3x4(h[i][0] * inv, h[i][1] * inv, h[i][2] * inv, h[i][3] * inv),
-            e4m3x4(h[i][4] * inv, h[i][5] * inv, h[i][6] * inv, h[i][7] * inv));
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[i][e] = scale_to_e4m3<false>(h[i][e], sc);
+        const uint2 q = make_uint2(e4m3x4(h[i][0], h[i][1], h[i][2], h[i][3]),
+                                   e4m3x4(h[i][4], h[i][5], h[i][6], h[i][7]));
         *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.y) + base + 8 * p) = q;
         if ((p & 15) == 0)
           a.scales[(size_t)row * ((a.cols + 127) >> 7) + (p >> 4)] = am / kE4m3Max;

@@ -141,7 +141,7 @@ __device__ __forceinline__ void quant_tile(const QuantArgs& a, unsigned block) {
   constexpr int kMags = Piece::kMags, kPerMag = 8 / kMags;
   __shared__ uint32_t cmax[8][128 / kPerMag];
   __shared__ float csum[8][128];
-  __shared__ float cinv[128], cam[128];
+  __shared__ float cinv[128], clo[128];
   __shared__ __align__(16) uint8_t tile[128 * 128];
   grid_dep_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, rg = tid >> 4, cg = tid & 15;
@@ -195,7 +195,7 @@ __device__ __forceinline__ void quant_tile(const QuantArgs& a, unsigned block) {
       if (!kSquare) {
         const int from = (lane & 16) + 2 * i;
         sc.inv = __shfl_sync(0xffffffffu, mine.inv, from);
-        if (!kBf16) sc.amax = __shfl_sync(0xffffffffu, mine.amax, from);
+        if (!kBf16) sc.lo = __shfl_sync(0xffffffffu, mine.lo, from);
       }
       float q[8];
 #pragma unroll
@@ -234,8 +234,9 @@ __device__ __forceinline__ void quant_tile(const QuantArgs& a, unsigned block) {
 #pragma unroll
         for (int i = 1; i < 8; ++i) m = Piece::max2(m, cmax[i][tid / kPerMag]);
         const float am = block_amax(Piece::column(m, tid));
-        cinv[tid] = kE4m3Max / am;
-        cam[tid] = am;
+        const BlockScale sc(am);
+        cinv[tid] = sc.inv;
+        clo[tid] = sc.lo;
         if (c < a.cols) a.scales_t[(size_t)c * ((a.rows + 127) >> 7) + tr] = am / kE4m3Max;
       }
     } else if (a.colsum && c < a.cols) {
@@ -252,7 +253,7 @@ __device__ __forceinline__ void quant_tile(const QuantArgs& a, unsigned block) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     const int c = 8 * cg + e;
-    const BlockScale sc = kSquare ? sq : BlockScale(cinv[c], cam[c]);
+    const BlockScale sc = kSquare ? sq : BlockScale(cinv[c], clo[c]);
     float q[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) q[i] = scale_to_e4m3<kBf16>(v[i].get(e), sc);
