@@ -317,7 +317,9 @@ LSH_API lsh_status lsh_rev_backward(const lsh_shape* shape, int32_t d_ff, int32_
  * or of 128 rows ([ceil(rows / 128), ceil(cols / 128)], "128 x 128"; the last
  * blocks of either axis may be short).  With m the block's largest magnitude,
  * 2^-96 at least, its scale is m / 448 and its codes are e4m3(448 v / m),
- * rounded to nearest even; it stands for code * scale.  A block that holds an
+ * rounded to nearest even (the quotient as exact arithmetic gives it for bf16,
+ * to the last bit of an fp32 for fp32 entries); it stands for code * scale.  A
+ * block that holds an
  * infinity or a NaN stands for NaN throughout.
  *
  * All sizes called cols, N, K, d_model and d_ff are multiples of 16

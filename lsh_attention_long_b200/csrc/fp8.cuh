@@ -52,19 +52,35 @@ struct BlockScale {
   }
   __device__ __forceinline__ BlockScale(float i, float l) : inv(i), lo(l) {}
 };
-template <bool kFromBf16>
-__device__ __forceinline__ float scale_to_e4m3(float v, const BlockScale& b) {
-  const float q = v * b.inv;
-  if (kFromBf16) return __uint_as_float((__float_as_uint(q) + 0x80u) & 0xffffff00u);
-  return q + fmaf(v, b.lo, fmaf(v, b.inv, -q));
-}
-
 // Two or four codes, the first in the lowest byte.
 __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
   return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
 }
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   return e4m3x2(a, b) | (e4m3x2(c, d) << 16);
+}
+
+// Codes of eight entries of a block, two at a time.  (A float is rounded to 16
+// bits as 257 q - (257 q - q).)
+template <bool kFromBf16>
+__device__ __forceinline__ uint2 scale_to_e4m3(const float* v, const BlockScale& b) {
+  const float2 inv = make_float2(b.inv, b.inv), lo = make_float2(b.lo, b.lo);
+  float2 q[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 x = make_float2(v[2 * i], v[2 * i + 1]);
+    q[i] = __fmul2_rn(x, inv);
+    if (kFromBf16) {
+      const float2 c = __fmul2_rn(q[i], make_float2(257.f, 257.f));
+      const float2 d = __ffma2_rn(q[i], make_float2(-1.f, -1.f), c);
+      q[i] = __ffma2_rn(d, make_float2(-1.f, -1.f), c);
+    } else {
+      const float2 rest = __ffma2_rn(x, inv, make_float2(-q[i].x, -q[i].y));
+      q[i] = __fadd2_rn(q[i], __ffma2_rn(x, lo, rest));
+    }
+  }
+  return make_uint2(e4m3x4(q[0].x, q[0].y, q[1].x, q[1].y),
+                    e4m3x4(q[2].x, q[2].y, q[3].x, q[3].y));
 }
 
 }  // namespace lsh

@@ -90,7 +90,8 @@ template <typename XT>
 lsh_status quant_launch(const lsh::QuantArgs& a, int block_rows, cudaStream_t st) {
   if (block_rows == 1 && !a.yt && !a.colsum) {
     const long long padded = ((a.cols >> 3) + 15) & ~15;
-    const long long grid = (a.rows * padded + 255) / 256;
+    constexpr int kPer = 256 * lsh::kQuantRowsPer<XT>;
+    const long long grid = (a.rows * padded + kPer - 1) / kPer;
     if (grid > 0x7fffffffLL) return LSH_ERR_UNSUPPORTED;
     return launch_pdl(lsh::quant_rows_kernel<XT>, dim3((unsigned)grid), dim3(256), 0, st, a);
   }
@@ -468,14 +469,16 @@ lsh_status lsh_matmul_fp8_backward(int32_t M, int32_t N, int32_t K, const void* 
   auto f = [&](size_t at) { return reinterpret_cast<float*>(w + at); };
   lsh::QuantArgs q = quant_args(M, N, dC, dA ? w + l.dc : nullptr, f(l.dc_s),
                                 dB ? w + l.dct : nullptr, f(l.dct_s));
-  q.colsum = db ? f(l.sums) : nullptr;
+  // one block of 128 rows: its column sums are db
+  const bool one = kblocks(M) == 1;
+  q.colsum = !db ? nullptr : one ? db : f(l.sums);
   // only what is asked for is put into 8 bits; db alone still reads dC once
   if (dB)
     s = quant_two_launch(q, quant_args(M, K, A, nullptr, nullptr, w + l.at, f(l.at_s)), st);
   else
     s = quant_launch<__nv_bfloat16>(q, 1, st);
   if (s != LSH_OK) return s;
-  if (db && (s = column_sum(f(l.sums), (int)kblocks(M), N, db, st)) != LSH_OK) return s;
+  if (db && !one && (s = column_sum(f(l.sums), (int)kblocks(M), N, db, st)) != LSH_OK) return s;
   if (dA) {
     lsh::Fp8GemmArgs g = fp8_gemm_args(M, K, N, w + l.dc, f(l.dc_s), Bt, bt_scales, 128);
     g.C = dA;

@@ -16,6 +16,11 @@
 // CTAs of a cluster share out a tile's K and add their totals up through
 // distributed shared memory.
 //
+// Measured: 8192 x 4096 x 4096 in 120 us (2 270 TFLOP/s, 61% of the tensor
+// cores' cycles; with column scales 167 us).  What is left is the exchange of
+// the two accumulators: each is written in 512 cycles, handed over in some 370
+// (commit, arrival, next issue) and read and added in 360 at best.
+//
 // Warp roles (384 threads, persistent blocks, one per SM):
 //   warp 0      one thread loads A and B tiles of 128-byte rows with TMA
 //               (128-byte swizzle; zeros past the matrices' ends) into a ring
