@@ -319,8 +319,7 @@ LSH_API lsh_status lsh_rev_backward(const lsh_shape* shape, int32_t d_ff, int32_
  * 2^-96 at least, its scale is m / 448 and its codes are e4m3(448 v / m),
  * rounded to nearest even (the quotient as exact arithmetic gives it for bf16,
  * to the last bit of an fp32 for fp32 entries); it stands for code * scale.  A
- * block that holds an
- * infinity or a NaN stands for NaN throughout.
+ * block that holds an infinity or a NaN stands for NaN throughout.
  *
  * All sizes called cols, N, K, d_model and d_ff are multiples of 16
  * (else LSH_ERR_UNSUPPORTED); numbers of rows, M and tokens are any.  The
@@ -368,14 +367,11 @@ LSH_API lsh_status lsh_quantize_fp8(int32_t rows, int32_t cols, int32_t x_dtype,
 /* C = A B^T + bias, then max(0, .) if relu: A [M, K] with 1 x 128 scales, B
  * [N, K] with 1 x 128 or 128 x 128 scales (b_block_rows), bias [N] bf16 or
  * NULL, C [M, N] fp32 or bf16 (c_dtype).  Products and sums are fp32; a
- * block's sum over K enters the total with its two scales.  ws: at least
- * lsh_matmul_fp8_ws_size() bytes of device scratch (0 where none is needed). */
-LSH_API size_t lsh_matmul_fp8_ws_size(int32_t M, int32_t N, int32_t K);
+ * block's sum over K enters the total with its two scales. */
 LSH_API lsh_status lsh_matmul_fp8(int32_t M, int32_t N, int32_t K, const void* A,
                                   const float* a_scales, const void* B, const float* b_scales,
                                   int32_t b_block_rows, const void* bias, int32_t relu,
-                                  int32_t c_dtype, void* C, void* ws, size_t ws_bytes,
-                                  void* stream);
+                                  int32_t c_dtype, void* C, void* stream);
 
 /* Gradients of C = A B^T + bias (without relu), the quantisers taken as
  * identities, with every product in 8 bits:

@@ -415,24 +415,17 @@ lsh_status lsh_quantize_fp8(int32_t rows, int32_t cols, int32_t x_dtype, int32_t
                              : quant_launch<float>(a, block_rows, as_stream(stream));
 }
 
-size_t lsh_matmul_fp8_ws_size(int32_t M, int32_t N, int32_t K) {
-  (void)M; (void)N; (void)K;
-  return 0;
-}
-
 lsh_status lsh_matmul_fp8(int32_t M, int32_t N, int32_t K, const void* A, const float* a_scales,
                           const void* B, const float* b_scales, int32_t b_block_rows,
-                          const void* bias, int32_t relu, int32_t c_dtype, void* C, void* ws,
-                          size_t ws_bytes, void* stream) {
+                          const void* bias, int32_t relu, int32_t c_dtype, void* C,
+                          void* stream) {
   if (!is_f32_or_bf16(c_dtype) || (b_block_rows != 1 && b_block_rows != 128))
     return LSH_ERR_INVALID_ARG;
   const lsh_status s = fp8_sizes_check(M, N, K);
   if (s != LSH_OK) return s;
   if (M == 0) return LSH_OK;
   if (!A || !a_scales || !B || !b_scales || !C) return LSH_ERR_INVALID_ARG;
-  if (any_misaligned({A, a_scales, B, b_scales, bias, C, ws})) return LSH_ERR_INVALID_ARG;
-  const size_t need = lsh_matmul_fp8_ws_size(M, N, K);
-  if (need && (!ws || ws_bytes < need)) return LSH_ERR_WORKSPACE;
+  if (any_misaligned({A, a_scales, B, b_scales, bias, C})) return LSH_ERR_INVALID_ARG;
   lsh::Fp8GemmArgs g = fp8_gemm_args(M, N, K, A, a_scales, B, b_scales, b_block_rows);
   g.bias = static_cast<const __nv_bfloat16*>(bias);
   g.relu = relu ? 1 : 0;

@@ -249,7 +249,7 @@ def lsh_quantize_fp8(X, *, block_rows: int = 1, transposed: bool = False, Y=None
 
 
 def lsh_matmul_fp8(A, a_scales, B, b_scales, *, bias=None, relu: bool = False,
-                   out_dtype=torch.bfloat16, C=None, ws=None, stream=None):
+                   out_dtype=torch.bfloat16, C=None, stream=None):
     """C [M, N] = A B^T (+ bias) (max(0, .) if ``relu``) of 8-bit matrices A [M, K] (1 x 128
     blocks) and B [N, K] (1 x 128 or 128 x 128 blocks, told by b_scales' shape), in fp32 or bf16."""
     M, K = _matrix("A", A, (F8,))
@@ -286,11 +286,10 @@ def lsh_matmul_fp8(A, a_scales, B, b_scales, *, bias=None, relu: bool = False,
     with _on(dev, stream):
         if C is None:
             C = A.new_empty((M, N), dtype=out_dtype)
-        ws, wp, wn = _scratch("lsh_matmul_fp8_ws_size", (M, N, K), ws, dev)
         _done("lsh_matmul_fp8", _lib().lsh_matmul_fp8(
             M, N, K, A.data_ptr(), a_scales.data_ptr(), B.data_ptr(),
             b_scales.data_ptr(), 1 if rowwise else 128, _p(bias), int(relu),
-            _CODES[out_dtype], C.data_ptr(), wp, wn, _raw_stream(dev)))
+            _CODES[out_dtype], C.data_ptr(), _raw_stream(dev)))
     return C
 
 

@@ -29,7 +29,7 @@ EXPORTS = ("lsh_workspace_size", "lsh_hash", "lsh_sort", "lsh_attend_fwd", "lsh_
            "lsh_ffn_ws_size", "lsh_ffn_forward", "lsh_ffn_bwd_ws_size", "lsh_ffn_backward",
            "lsh_rev_ws_size", "lsh_rev_forward", "lsh_rev_backward",
            "lsh_rmsnorm_forward", "lsh_rmsnorm_bwd_ws_size", "lsh_rmsnorm_backward",
-           "lsh_quantize_fp8", "lsh_matmul_fp8_ws_size", "lsh_matmul_fp8",
+           "lsh_quantize_fp8", "lsh_matmul_fp8",
            "lsh_matmul_fp8_bwd_ws_size", "lsh_matmul_fp8_backward", "lsh_ffn_fp8_ws_size",
            "lsh_ffn_forward_fp8")
 
@@ -85,8 +85,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "lsh_rmsnorm_bwd_ws_size": ([I] * 2, sz),
         "lsh_rmsnorm_backward": ([I] * 5 + [P] * 8 + [sz, P], ctypes.c_int),
         "lsh_quantize_fp8": ([I] * 4 + [P] * 6, ctypes.c_int),
-        "lsh_matmul_fp8_ws_size": ([I] * 3, sz),
-        "lsh_matmul_fp8": ([I] * 3 + [P] * 4 + [I, P, I, I, P, P, sz, P], ctypes.c_int),
+        "lsh_matmul_fp8": ([I] * 3 + [P] * 4 + [I, P, I, I, P, P], ctypes.c_int),
         "lsh_matmul_fp8_bwd_ws_size": ([I] * 3, sz),
         "lsh_matmul_fp8_backward": ([I] * 3 + [P] * 4 + [I] + [P] * 4 + [sz, P], ctypes.c_int),
         "lsh_ffn_fp8_ws_size": ([I] * 4, sz),

@@ -124,7 +124,7 @@ def test_quantizer_abi(lib):
 
 def test_product_abi(lib):
     def mm(M=4, N=32, K=64, A=P, sa=P, Bm=P, sb=P, br=128, bias=None, c=1, C=P):
-        return lib.lsh_matmul_fp8(M, N, K, A, sa, Bm, sb, br, bias, 0, c, C, None, 0, None)
+        return lib.lsh_matmul_fp8(M, N, K, A, sa, Bm, sb, br, bias, 0, c, C, None)
     for kw in (dict(M=-1), dict(N=0), dict(K=0), dict(br=64), dict(c=2), dict(A=None),
                dict(sa=None), dict(Bm=None), dict(sb=None), dict(C=None),
                dict(bias=ctypes.c_void_p(4098)), dict(A=ctypes.c_void_p(4104))):
