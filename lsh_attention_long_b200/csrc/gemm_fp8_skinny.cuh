@@ -63,6 +63,8 @@ __global__ void __launch_bounds__(32 * kW) gemm_fp8_skinny_kernel(Fp8SkinnyArgs 
   const int gr = lane >> 2, tc4 = lane & 3;
   const int n0 = blockIdx.x * kRows;
   const int n_c = (g.K + 63) >> 6, kbs = (g.K + 127) >> 7;
+  // shared memory of another CTA may be written only once that CTA has started
+  if (kEpi == kF8Quant) tc::cluster_arrive_relaxed();
   if (!a.early_b) grid_dep_wait();
   float acc[kRG][kNT][4] = {};
   bool waited = !a.early_b;
@@ -169,6 +171,7 @@ __global__ void __launch_bounds__(32 * kW) gemm_fp8_skinny_kernel(Fp8SkinnyArgs 
     // block of the cluster
     constexpr int kCluster = 128 / kRows;
     const uint32_t rank = tc::cluster_rank();
+    tc::cluster_wait();
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int o = tid + i * kSkThreads, m = o / kRows;

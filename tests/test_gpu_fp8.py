@@ -380,14 +380,16 @@ def test_ffn(T, D, F, chunk):
     close(Y, want, tol + HALF[BF] * (want.abs() + tol), "Y")
 
 
-@pytest.mark.parametrize("T,D,F,chunk", [(9000, 64, 8208, 128), (20000, 128, 4112, 4096)])
+@pytest.mark.parametrize("T,D,F,chunk", [(9000, 64, 8208, 128), (20000, 128, 4112, 4096),
+                                         (257, 64, 131088, 128)])  # the last chunk one position
 def test_ffn_of_several_chunks(T, D, F, chunk):
     """Enough positions for three chunks and more, whose products overlap from launch to launch and
     take turns on two buffers: the same as each position's own row of one call on it alone, up to
     the order of fp32 sums, and the same bits on every run."""
     s = ffn_state(T, D, F)
     ws = L.ffn_fp8_workspace(T, D, F, chunk, torch.device("cuda"))
-    assert ws.numel() < 2.2 * (max(32 << 20, chunk * F) + (1 << 20)) < T * F * 2
+    assert T > 2 * max(chunk, (32 << 20) // F // 256 * 256)  # three chunks
+    assert ws.numel() < 2.2 * (max(32 << 20, chunk * F) + (1 << 20))
     ws.fill_(0x7f)  # NaN wherever something is read before it is written
     first = ffn(s, chunk, ws=ws).clone()
     ok()
@@ -395,7 +397,7 @@ def test_ffn_of_several_chunks(T, D, F, chunk):
     for _ in range(10):
         assert torch.equal(ffn(s, chunk, ws=ws), first)
     ok()
-    rows = torch.arange(0, T, 97, device="cuda")
+    rows = torch.cat([torch.arange(0, T, 97), torch.tensor([T - 1])]).cuda()
     part = dict(s, X8=s["X8"].view(torch.uint8)[rows].view(F8), sx=s["sx"][rows])
     alone = ffn(part, chunk).double()
     # a sum in another order may put a hidden entry on the next code: 2^-4 of it, one in
@@ -475,6 +477,56 @@ def test_another_stream(T):
         assert torch.equal(Y, want) and all(torch.equal(x, y) for x, y in zip(b, want_b))
         del junk
     ok()
+
+
+def test_two_calls_at_once():
+    """Feed-forwards of several chunks and products on two streams at the same time, each with its
+    own workspace, give what they give alone."""
+    T, D, F = 9000, 128, 4112
+    states = [ffn_state(T, D, F, seed) for seed in (1, 2)]
+    want = [ffn(s, 128) for s in states]
+    few = [ffn(dict(s, X8=s["X8"][:3], sx=s["sx"][:3]), 128) for s in states]
+    ok()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(5):
+        for i, (s, st) in enumerate(zip(states, streams)):
+            got[i].append((ffn(s, 128, stream=st),
+                           ffn(dict(s, X8=s["X8"][:3], sx=s["sx"][:3]), 128, stream=st)))
+    ok()
+    for i in range(2):
+        assert all(torch.equal(y, want[i]) and torch.equal(z, few[i]) for y, z in got[i])
+
+
+@pytest.mark.parametrize("T", [1, 3, 16, 40, 300])
+def test_inputs_written_just_before(T):
+    """Every input put into 8 bits anew right before the call that reads it, without a pause
+    between them: no product reads what was there before."""
+    D, F = 256, 1040
+    g = gen(T)
+    b1, b2 = rnd(g, F, t=BF), rnd(g, D, t=BF)
+    sets = [(rnd(g, T, D), rnd(g, F, D), rnd(g, D, F)) for _ in range(2)]
+    e = lambda *sh, t=F32: torch.empty(*sh, dtype=t, device="cuda")  # noqa: E731
+    x8, sx = e(T, D, t=F8), e(T, D // 128)
+    w1, s1, w2, s2 = e(F, D, t=F8), e(9, 2), e(D, F, t=F8), e(2, 9)
+
+    def run(X, W1, W2):
+        L.lsh_quantize_fp8(X, Y=x8, scales=sx)
+        L.lsh_quantize_fp8(W1, block_rows=128, Y=w1, scales=s1)
+        L.lsh_quantize_fp8(W2, block_rows=128, Y=w2, scales=s2)
+        Y = L.lsh_ffn_forward_fp8(x8, sx, w1, s1, b1, w2, s2, b2, 128)
+        L.lsh_quantize_fp8(W1, block_rows=128, Y=w1, scales=s1)  # over what was just read
+        return Y, L.lsh_matmul_fp8(x8, sx, w1, s1)
+
+    want = []
+    for t in sets:
+        want.append([y.clone() for y in run(*t)])
+        ok()
+    assert not torch.equal(want[0][0], want[1][0])
+    got = [run(*sets[i & 1]) for i in range(40)]
+    ok()
+    for i, ys in enumerate(got):
+        assert all(torch.equal(y, w) for y, w in zip(ys, want[i & 1]))
 
 
 def test_empty_calls():
