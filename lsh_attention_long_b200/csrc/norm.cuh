@@ -293,9 +293,8 @@ __global__ void __launch_bounds__(norm_block(kT)) rmsnorm_bwd_kernel(NormBwdArgs
 // out[c] = sum over b of part[b][c]: a block sums 32 columns, its 32 warps
 // every 32nd row each, eight loads under way at a time, and adds the warps up
 // in a fixed order.
-__global__ void __launch_bounds__(1024) column_sum_kernel(const float* __restrict__ part,
-                                                          int blocks, int cols,
-                                                          float* __restrict__ out) {
+__global__ void __launch_bounds__(1024) column_sum_kernel(const float* part, int blocks, int cols,
+                                                          float* out) {
   __shared__ float red[32][33];
   grid_dep_wait();
   grid_dep_launch();
