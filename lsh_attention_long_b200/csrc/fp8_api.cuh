@@ -175,16 +175,28 @@ lsh_status fp8_tc_launch(const lsh::Fp8TcArgs& a, cudaStream_t st) {
                             dim3(lsh::kF8Threads), smem, st, kPair * kParts, ma, mb, mc, a);
 }
 
-template <int kNT, int kRG, int kW, int kEpi>
+template <int kNT, int kW, int kEpi>
 lsh_status fp8_skinny_launch(const lsh::Fp8SkinnyArgs& a, cudaStream_t st) {
   // a cluster covers 128 rows of B, one block of the 8-bit result
-  constexpr int kRows = 16 * kRG, kCluster = kEpi == lsh::kF8Quant ? 128 / kRows : 1;
-  const int grid = ceil_div(ceil_div(a.g.N, kRows), kCluster) * kCluster;
-  return launch_pdl_cluster(lsh::gemm_fp8_skinny_kernel<kNT, kRG, kW, kEpi>, dim3((unsigned)grid),
-                            dim3(32 * kW), 0, st, kCluster, a);
+  constexpr int kCluster = kEpi == lsh::kF8Quant ? 128 / lsh::kSkRows : 1;
+  const int grid = ceil_div(ceil_div(a.g.N, lsh::kSkRows), kCluster) * kCluster;
+  const auto kernel = lsh::gemm_fp8_skinny_kernel<kNT, kW, kEpi>;
+  constexpr size_t smem = lsh::sk_smem_bytes(kW);
+  const lsh_status s = allow_smem(kernel, smem);
+  if (s != LSH_OK) return s;
+  return launch_pdl_cluster(kernel, dim3((unsigned)grid), dim3(32 * kW), smem, st, kCluster, a);
 }
-// Blocks of 4 warps where there are two or more for every SM, else of 8, which
-// read a row group in half the time.
+// Warps per block of 16 rows: eight, which are through K soonest, while blocks
+// are few; fewer where several blocks share an SM, so that the last ones to
+// start leave less idle (one row, 16 384 x 8192: 28 us with two, 32 with four;
+// 8192 x 2048: 6.2 with four, 6.5 with eight).
+template <int kNT, int kEpi>
+lsh_status fp8_skinny_launch(const lsh::Fp8SkinnyArgs& a, cudaStream_t st) {
+  const int per_sm = ceil_div(a.g.N, lsh::kSkRows) / num_sms();
+  if (per_sm >= 4) return fp8_skinny_launch<kNT, 2, kEpi>(a, st);
+  if (per_sm >= 2) return fp8_skinny_launch<kNT, 4, kEpi>(a, st);
+  return fp8_skinny_launch<kNT, 8, kEpi>(a, st);
+}
 template <int kEpi>
 lsh_status fp8_skinny_launch(const lsh::Fp8GemmArgs& g, void* Q, float* qs, int early_b,
                              cudaStream_t st) {
@@ -193,11 +205,7 @@ lsh_status fp8_skinny_launch(const lsh::Fp8GemmArgs& g, void* Q, float* qs, int 
   a.Q = static_cast<uint8_t*>(Q);
   a.qs = qs;
   a.early_b = early_b;
-  const int rows = g.M <= 8 ? 16 : 32;
-  const bool many = ceil_div(g.N, rows) >= 2 * num_sms();
-  if (g.M <= 8)
-    return many ? fp8_skinny_launch<1, 1, 4, kEpi>(a, st) : fp8_skinny_launch<1, 1, 8, kEpi>(a, st);
-  return many ? fp8_skinny_launch<2, 2, 4, kEpi>(a, st) : fp8_skinny_launch<2, 2, 8, kEpi>(a, st);
+  return g.M <= 8 ? fp8_skinny_launch<1, kEpi>(a, st) : fp8_skinny_launch<2, kEpi>(a, st);
 }
 
 // Whether 256 x 256 tiles, on a pair of CTAs each, are enough to occupy half of
@@ -229,14 +237,7 @@ lsh_status fp8_tc_gemm(const lsh::Fp8TcArgs& a, cudaStream_t st) {
   return fp8_tc_launch<1, 128, lsh::kF8Store, kColScale, 1>(a, st);
 }
 
-// Whether the kernel for few rows is the faster one.  Its MMAs take 8 rows at a
-// time, so from 9 on it needs twice as many and falls behind where they, not
-// the trip to memory, are the larger part: 16 x 2048 x 512 takes 3.6 us with it
-// and 4.0 with tcgen05 tiles, 16 x 4096 x 4096 14.4 and 10.3 (8 rows: 7.3 and
-// 10.3).
-bool fp8_few_rows(const lsh::Fp8GemmArgs& g) {
-  return g.M <= 8 || (g.M <= lsh::kSkMaxM && g.K <= 1024 && g.N <= 8192);
-}
+bool fp8_few_rows(const lsh::Fp8GemmArgs& g) { return g.M <= lsh::kSkMaxM; }
 
 // early_b: see Fp8SkinnyArgs.
 lsh_status fp8_gemm_launch(const lsh::Fp8GemmArgs& g, cudaStream_t st, int order = lsh::kF8Wait,

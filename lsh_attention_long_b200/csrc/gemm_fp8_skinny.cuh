@@ -3,18 +3,21 @@
 // Such a product reads B once and does little else, so it is bound by memory,
 // or at small sizes by one trip to memory and back.  A 128-row tcgen05 tile
 // would be mostly zeros and starts late (tensor memory, descriptors, a
-// pipeline to fill); here B streams from memory into registers, already in the
-// fragment layout of mma.sync m16n8k32 (B's rows are its 16 rows, A's rows its
-// 8 columns): a lane's 16 bytes of a row serve two MMAs, with the codes of K
-// taken in the same permuted order from both operands.  (The same through
-// fp16, converted first, m16n8k16: 8.5 us in place of 6.7 at 1 x 8192 x 2048.)
+// pipeline to fill); here B streams through a ring in shared memory (cp.async:
+// what is in flight costs no registers) in pieces of 16 bytes that a lane
+// brings for itself, already in the fragment layout of mma.sync m16n8k32 (B's
+// rows are its 16 rows, A's rows its 8 columns): a piece serves two MMAs, with
+// the codes of K taken in the same permuted order from both operands.  (One row:
+// 8192 x 2048 6.1 us, 16 384 x 8192 27 us, 4.9 TB/s; with loads into registers,
+// which wait between batches, 6.7 and 39; these and codes converted to fp16
+// first, m16n8k16, 8.9 and 53.  16 rows: 7.9 and 35 us, tcgen05 tiles 8.8 and
+// 39.)
 //
-// A block of kW warps has kRG groups of 16 rows of B; its warps share out K in
-// chunks of 64, scale each chunk's sum (its block of 128 has one scale) into
-// fp32 totals, and add the totals up through shared memory in a fixed order.
-// To put the result into 8 bits (1 x 128 blocks along B's rows), the blocks of
-// a cluster, 128 rows of B together, exchange their largest magnitudes through
-// distributed shared memory.
+// A block of kW warps has 16 rows of B; its warps share out K in chunks of 128,
+// scale each chunk's sum into fp32 totals, and add the totals up through shared
+// memory in a fixed order.  To put the result into 8 bits (1 x 128 blocks along
+// B's rows), the eight blocks of a cluster, 128 rows of B together, exchange
+// their largest magnitudes through distributed shared memory.
 #pragma once
 
 #include "gemm_fp8_tc.cuh"
@@ -41,105 +44,131 @@ __device__ __forceinline__ void mma_sync_e4m3(float* c, uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// (Not .nc: the grid may have started before the one that wrote the data ended.)
-__device__ __forceinline__ uint4 load16_stream(const uint8_t* p) {
-  uint4 v;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
+// 16 bytes into shared memory, asynchronously; zeros if !in.  (Through L2, as
+// the grid may have started before the one that wrote the data ended.)
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(in ? 16 : 0)
+               : "memory");
 }
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+constexpr int kSkRows = 16;
+// Chunks in flight per warp (2 KB each; three or six: no faster), and the
+// shared memory for them.
+constexpr int kSkDeep = 4;
+constexpr size_t sk_smem_bytes(int kW) { return (size_t)kSkDeep * kW * 2048; }
 
-// kNT: column tiles of 8 (rows of A); kRG: groups of 16 rows of B per block;
-// kW: warps per block.
-template <int kNT, int kRG, int kW, int kEpi>
+// kNT: column tiles of 8 (rows of A); kW: warps per block.
+template <int kNT, int kW, int kEpi>
 __global__ void __launch_bounds__(32 * kW) gemm_fp8_skinny_kernel(Fp8SkinnyArgs a) {
   constexpr int kSkThreads = 32 * kW;
-  constexpr int kDeep = kNT == 1 ? 4 : 2;  // chunks in flight per warp
-  constexpr int kRows = 16 * kRG, kTok = 8 * kNT;
+  constexpr int kRows = kSkRows, kTok = 8 * kNT;
   __shared__ float red[kW][kRows][kTok + 1];
   __shared__ float cmax[128 / kRows][kTok];
   const Fp8GemmArgs& g = a.g;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int gr = lane >> 2, tc4 = lane & 3;
   const int n0 = blockIdx.x * kRows;
-  const int n_c = (g.K + 63) >> 6, kbs = (g.K + 127) >> 7;
+  const int n_c = (g.K + 127) >> 7;
   // shared memory of another CTA may be written only once that CTA has started
   if (kEpi == kF8Quant) tc::cluster_arrive_relaxed();
   if (!a.early_b) grid_dep_wait();
-  float acc[kRG][kNT][4] = {};
-  bool waited = !a.early_b;
-  for (int c0 = warp; c0 < n_c; c0 += kW * kDeep) {
-    uint4 wv[kDeep][kRG][2];
+  // a lane's own pieces [chunk in flight][row][half of the chunk]: nobody else
+  // reads them, so the warps need no barrier
+  extern __shared__ __align__(16) uint8_t ring[];
+  constexpr uint32_t kPiece = kSkThreads * 16, kSlot = 4 * kPiece;
+  uint8_t* const mine = ring + tid * 16;
+  const uint32_t mine_at = tc::smem_u32(mine);
+  const uint8_t* pb[2];  // rows n0 + gr and n0 + 8 + gr
+  const float* psb[2];
 #pragma unroll
-    for (int d = 0; d < kDeep; ++d) {
-      const int k = (c0 + kW * d) * 64 + 16 * tc4;
+  for (int h = 0; h < 2; ++h) {
+    const int n = n0 + 8 * h + gr;
+    pb[h] = n < g.N ? g.B + (size_t)n * g.K + 16 * tc4 : nullptr;
+    psb[h] = g.sb + (size_t)(n < g.N ? n / g.b_rows : 0) * n_c;
+  }
+  const auto fetch = [&](int c, int slot) {
+    if (c < n_c) {
 #pragma unroll
-      for (int r = 0; r < kRG; ++r)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int n = n0 + 16 * r + 8 * h + gr;
-          wv[d][r][h] = make_uint4(0, 0, 0, 0);
-          if (k < g.K && n < g.N) wv[d][r][h] = load16_stream(g.B + (size_t)n * g.K + k);
-        }
-    }
-    if (!waited) {
-      grid_dep_wait();
-      waited = true;
-    }
-    uint4 av[kDeep][kNT];
-    float sa[kDeep][kNT][2], sb[kDeep][kRG][2];
-#pragma unroll
-    for (int d = 0; d < kDeep; ++d) {
-      // past the end of K the codes are zero, and any scale will do
-      const int c = c0 + kW * d, kb = c < n_c ? c >> 1 : 0;
-      const int k = c * 64 + 16 * tc4;
-#pragma unroll
-      for (int t = 0; t < kNT; ++t) {
-        const int m = 8 * t + gr;
-        av[d][t] = make_uint4(0, 0, 0, 0);
-        if (k < g.K && m < g.M)
-          av[d][t] = *reinterpret_cast<const uint4*>(g.A + (size_t)m * g.K + k);
+      for (int half = 0; half < 2; ++half) {
+        const int k = c * 128 + 64 * half;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int ms = 8 * t + 2 * tc4 + h;
-          sa[d][t][h] = ms < g.M ? g.sa[(size_t)ms * kbs + kb] : 0.f;
+          const bool in = pb[h] && k + 16 * tc4 < g.K;
+          copy16(mine_at + slot * kSlot + (2 * h + half) * kPiece, in ? pb[h] + k : g.B, in);
         }
       }
+    }
+    copy_commit();
+  };
 #pragma unroll
-      for (int r = 0; r < kRG; ++r)
+  for (int d = 0; d < kSkDeep; ++d) fetch(warp + kW * d, d);
+  if (a.early_b) grid_dep_wait();
+  struct Side {  // what a chunk needs of A, and the scales, a chunk ahead
+    uint4 av[kNT][2];
+    float sa[kNT][2], sb[2];
+  } next;
+  const auto load_side = [&](int c) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int n = n0 + 16 * r + 8 * h + gr;
-          sb[d][r][h] = g.sb[(size_t)(n < g.N ? n / g.b_rows : 0) * kbs + kb];
-        }
+    for (int t = 0; t < kNT; ++t) {
+      const int m = 8 * t + gr;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int k = c * 128 + 64 * half + 16 * tc4;
+        next.av[t][half] = make_uint4(0, 0, 0, 0);
+        if (k < g.K && m < g.M)
+          next.av[t][half] = *reinterpret_cast<const uint4*>(g.A + (size_t)m * g.K + k);
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int ms = 8 * t + 2 * tc4 + h;
+        next.sa[t][h] = ms < g.M ? g.sa[(size_t)ms * n_c + c] : 0.f;
+      }
     }
 #pragma unroll
-    for (int d = 0; d < kDeep; ++d) {
-      if (c0 + kW * d >= n_c) break;
+    for (int h = 0; h < 2; ++h) next.sb[h] = psb[h][c];
+  };
+  float acc[kNT][4] = {};
+  if (warp < n_c) load_side(warp);
+  int slot = 0;
+  for (int c = warp; c < n_c; c += kW) {
+    const Side now = next;
+    if (c + kW < n_c) load_side(c + kW);
+    copy_wait<kSkDeep - 1>();
+    uint4 w[2][2];
 #pragma unroll
-      for (int t = 0; t < kNT; ++t)
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int r = 0; r < kRG; ++r) {
-          float p[4] = {0.f, 0.f, 0.f, 0.f};
-          const uint4 lo = wv[d][r][0], hi = wv[d][r][1], x = av[d][t];
-          mma_sync_e4m3(p, lo.x, hi.x, lo.y, hi.y, x.x, x.y);
-          mma_sync_e4m3(p, lo.z, hi.z, lo.w, hi.w, x.z, x.w);
+      for (int half = 0; half < 2; ++half)
+        w[h][half] =
+            *reinterpret_cast<const uint4*>(mine + slot * kSlot + (2 * h + half) * kPiece);
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            acc[r][t][e] = fmaf(p[e], sa[d][t][e & 1] * sb[d][r][e >> 1], acc[r][t][e]);
-        }
-    }
-  }
-  if (!waited) grid_dep_wait();
-  grid_dep_launch();
+    for (int t = 0; t < kNT; ++t) {
+      float p[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int r = 0; r < kRG; ++r)
-#pragma unroll
-    for (int t = 0; t < kNT; ++t)
+      for (int half = 0; half < 2; ++half) {
+        const uint4 lo = w[0][half], hi = w[1][half], x = now.av[t][half];
+        mma_sync_e4m3(p, lo.x, hi.x, lo.y, hi.y, x.x, x.y);
+        mma_sync_e4m3(p, lo.z, hi.z, lo.w, hi.w, x.z, x.w);
+      }
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        red[warp][16 * r + gr + 8 * (e >> 1)][8 * t + 2 * tc4 + (e & 1)] = acc[r][t][e];
+        acc[t][e] = fmaf(p[e], now.sa[t][e & 1] * now.sb[e >> 1], acc[t][e]);
+    }
+    // the MMAs have read the slot's pieces
+    fetch(c + kW * kSkDeep, slot);
+    slot = slot + 1 == kSkDeep ? 0 : slot + 1;
+  }
+  grid_dep_launch();
+#pragma unroll
+  for (int t = 0; t < kNT; ++t)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      red[warp][gr + 8 * (e >> 1)][8 * t + 2 * tc4 + (e & 1)] = acc[t][e];
   __syncthreads();
   // thread (token, row): neighbouring lanes have neighbouring rows of B, the
   // output's columns

@@ -261,7 +261,9 @@ PRODUCTS = [(1, 16, 16), (1, 144, 272), (3, 512, 2048), (8, 4096, 128), (9, 256,
             (2049, 528, 208),
             # pairs of CTAs on 256 x 256 tiles; K shared by 8, 4 and 2 CTAs; few rows, long K
             (2500, 1040, 400), (8200, 272, 128), (300, 640, 2064), (64, 4096, 3088),
-            (256, 4096, 4112), (12, 512, 1040), (16, 272, 4096)]
+            (256, 4096, 4112), (12, 512, 1040), (16, 272, 4096),
+            # few rows, many blocks of 16 of B's
+            (1, 9488, 656), (8, 4752, 400), (13, 4752, 1040), (16, 9488, 272)]
 
 
 @pytest.mark.parametrize("M,N,K", PRODUCTS)
@@ -352,7 +354,8 @@ def ffn(s, chunk, **kw):
                                          (16, 272, 1040, 128), (17, 128, 400, 128),
                                          (129, 256, 512, 128), (300, 144, 656, 256),
                                          (1000, 512, 2048, 384), (2048, 768, 1024, 8192),
-                                         (2500, 272, 1040, 8192), (12, 1040, 272, 128)])
+                                         (2500, 272, 1040, 8192), (12, 1040, 272, 128),
+                                         (3, 272, 4752, 128), (16, 128, 9616, 128)])
 def test_ffn(T, D, F, chunk):
     s = ffn_state(T, D, F)
     Y, intact = guarded((T, D), BF)
