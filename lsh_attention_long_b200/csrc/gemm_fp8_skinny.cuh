@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(32 * kW) gemm_fp8_skinny_kernel(Fp8SkinnyArgs 
       for (int s = kRows / 2; s; s >>= 1) b = max(b, __shfl_xor_sync(0xffffffffu, b, s));
       if (o < kOut && o % kRows < kCluster) {
         const uint32_t at = tc::cluster_map(tc::smem_u32(&cmax[rank][m]), (uint32_t)(o % kRows));
-        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(b) : "memory");
+        tc::st_cluster(at, b);
       }
     }
     tc::cluster_sync();

@@ -106,6 +106,7 @@ struct Fp8Smem {
   uint64_t acc_full[C::kBufs], acc_empty[C::kBufs];
   uint64_t sc_full[kF8Slots], sc_empty[kF8Slots];
   uint64_t mma_done[2];
+  uint32_t issued[2];  // by MMA warp: its first block of K that was not issued (in both CTAs)
   uint32_t amax[2][kEpi == kF8Quant && kBN == 128 ? kF8BM : 1];
   uint32_t tmem_base;
   int abort;
@@ -141,6 +142,25 @@ __device__ __forceinline__ bool f8_any(bool pred) {
       : "r"((uint32_t)pred)
       : "memory");
   return r != 0;
+}
+
+// About a millisecond.
+__device__ __forceinline__ void f8_pause() {
+  const long long t0 = clock64();
+  while (clock64() - t0 < 2000000) {
+  }
+}
+
+// The last block of K that went through barrier `at` of a ring of n, of those
+// that the MMA warps issued (warp w the blocks w, w + 2, .. before issued[w]); -1: none.
+__host__ __device__ inline int f8_last_block(const uint32_t* issued, int n, int at) {
+  int last = -1;
+  for (int w = 0; w < 2; ++w) {
+    int q = (int)issued[w] - 2;
+    for (int i = 0; i < n && q >= 0 && q % n != at; ++i) q -= 2;
+    if (q >= 0 && q % n == at && q > last) last = q;
+  }
+  return last;
 }
 
 template <int kPair, int kBN, int kEpi, bool kColScale, int kParts>
@@ -244,9 +264,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
       // After an abort one rank may have issued loads that the other's barrier
       // does not expect; then both give them time, far more than a load takes.
       if (kPair == 2 && *(volatile int*)&S.abort) {
-        const long long t0 = clock64();
-        while (clock64() - t0 < 2000000) {
-        }
+        f8_pause();
       } else {
         const uint32_t first = rank ? q : q > (uint32_t)kStages ? q - kStages : 0;
         for (uint32_t p = first; p < q; ++p)
@@ -263,7 +281,8 @@ __global__ void __launch_bounds__(kF8Threads, 1)
       constexpr uint32_t idesc = tc::idesc_e4m3(kPair * kF8BM, kBN);
       // all the blocks of this CTA's tiles, one after the other
       const uint32_t n_q = (n_units - first_unit + unit_step - 1) / unit_step * (uint32_t)n_k;
-      for (uint32_t q = warp - 1; q < n_q; q += 2) {
+      uint32_t q = warp - 1;
+      for (; q < n_q; q += 2) {
           const int s = q % kStages, b = q % kBufs;
           bool ok = f8_wait(&S.full[s], (q / kStages) & 1u, &S.abort, limit);
           const uint64_t da = tc::sdesc_sw128(tc::smem_u32(stage_a + s * C::kABytes), 16, 1024);
@@ -289,6 +308,9 @@ __global__ void __launch_bounds__(kF8Threads, 1)
       if (tc::elect_one()) {
         commit(&S.mma_done[warp - 1]);
         if (!tc::mbar_wait(&S.mma_done[warp - 1], 0)) record_status(tc::kErrTimeout);
+        S.issued[warp - 1] = q;
+        if (kPair == 2)
+          tc::st_cluster(tc::cluster_map(tc::smem_u32(&S.issued[warp - 1]), 1), q);
       }
     }
     __syncwarp();
@@ -616,7 +638,30 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   }
   tc::fence_before_sync();
   __syncthreads();
-  if (kPair == 2) tc::cluster_sync();  // neither leaves while the other may still reach it
+  if (kPair == 2) tc::cluster_sync();  // neither leaves while the other's threads may reach it
+  if (warp == 0) {
+    // Nor while a commit's arrival is on its way, which no barrier between
+    // threads orders: the last one on each barrier, one to a lane (of a pair in
+    // both CTAs, the commits being the even rank's).  A phase of a barrier
+    // follows another only once that one was seen in this CTA.  After an abort
+    // the epilogue waits for nothing and two may be on their way: then they get
+    // time as well, far more than an arrival takes.
+    if (*(volatile int*)&S.abort) f8_pause();
+    uint64_t* bar = nullptr;
+    uint32_t parity = 0;
+    const auto wait_for_last = [&](uint64_t* bars, int n, int at) {
+      const int last = f8_last_block(S.issued, n, at);
+      if (last >= 0) bar = bars + at;
+      parity = (uint32_t)(last / n) & 1u;
+    };
+    if (lane < kStages)
+      wait_for_last(S.empty, kStages, lane);
+    else if (lane < kStages + kBufs)
+      wait_for_last(S.acc_full, kBufs, lane - kStages);
+    else if (lane < kStages + kBufs + 2)
+      bar = S.mma_done + (lane - kStages - kBufs);
+    if (bar && !tc::mbar_wait(bar, parity)) record_status(tc::kErrTimeout);
+  }
   if (warp == 1) {
     tc::fence_after_sync();
     if (kPair == 2)

@@ -273,6 +273,9 @@ __device__ __forceinline__ void st_cluster(uint32_t cluster_addr, const float* v
                "f"(v[1]), "f"(v[2]), "f"(v[3])
                : "memory");
 }
+__device__ __forceinline__ void st_cluster(uint32_t cluster_addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
+}
 // Every thread of every CTA of the cluster.
 __device__ __forceinline__ void cluster_sync() {
   asm volatile(

@@ -608,3 +608,24 @@ def test_gradients_asked_for_one_by_one():
             ws.data_ptr(), n, ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
         ok()
         assert rc == 0 and torch.equal(out, want[which])
+
+
+@pytest.mark.parametrize("K", [16, 144, 400, 656])
+@pytest.mark.parametrize("b_rows", [1, 128])
+def test_pairs_of_ctas_that_leave_at_once(K, b_rows):
+    """Products on pairs of CTAs whose last blocks of K are their only ones, again and again without
+    a pause: a barrier's last arrival belongs to the grid that waits for it, not to the next one on
+    the same SM."""
+    g = gen(K)
+    A, sa = codes(g, 2500, K, 1)
+    B, sb = codes(g, 1040, K, b_rows)
+    want, size = product(ref.values(A, sa), ref.values(B, sb, b_rows))
+    first = L.lsh_matmul_fp8(A, sa, B, sb, out_dtype=F32)
+    ok()
+    close(first, want, sum_tol(K) * size + HALF[F32] * want.abs())
+    outs = [torch.empty_like(first) for _ in range(4)]
+    for _ in range(25):
+        for C in outs:
+            L.lsh_matmul_fp8(A, sa, B, sb, out_dtype=F32, C=C)
+        ok()
+        assert all(torch.equal(C, first) for C in outs)
