@@ -395,8 +395,8 @@ LSH_API lsh_status lsh_matmul_fp8_backward(int32_t M, int32_t N, int32_t K, cons
  * Y bf16; q(.) is 1 x 128 blocks of the fp32 hidden activation.  It works
  * through the positions `chunk` at a time (a multiple of 128), or more where
  * the hidden activation of those stays within 32 MB, so that the hidden
- * activation exists for two such chunks at most, the one being made and the one
- * being read (in ws, at least lsh_ffn_fp8_ws_size() bytes).  The chunk changes
+ * activation exists for two such chunks at most (in ws, at least
+ * lsh_ffn_fp8_ws_size() bytes, on which they take turns).  The chunk changes
  * the result only through the order of the fp32 sums. */
 LSH_API size_t lsh_ffn_fp8_ws_size(int32_t tokens, int32_t d_model, int32_t d_ff, int32_t chunk);
 LSH_API lsh_status lsh_ffn_forward_fp8(int32_t tokens, int32_t d_model, int32_t d_ff,

@@ -198,13 +198,11 @@ lsh_status fp8_skinny_launch(const lsh::Fp8SkinnyArgs& a, cudaStream_t st) {
   return fp8_skinny_launch<kNT, 8, kEpi>(a, st);
 }
 template <int kEpi>
-lsh_status fp8_skinny_launch(const lsh::Fp8GemmArgs& g, void* Q, float* qs, int early_b,
-                             cudaStream_t st) {
+lsh_status fp8_skinny_launch(const lsh::Fp8GemmArgs& g, void* Q, float* qs, cudaStream_t st) {
   lsh::Fp8SkinnyArgs a = {};
   a.g = g;
   a.Q = static_cast<uint8_t*>(Q);
   a.qs = qs;
-  a.early_b = early_b;
   return g.M <= 8 ? fp8_skinny_launch<1, kEpi>(a, st) : fp8_skinny_launch<2, kEpi>(a, st);
 }
 
@@ -239,28 +237,23 @@ lsh_status fp8_tc_gemm(const lsh::Fp8TcArgs& a, cudaStream_t st) {
 
 bool fp8_few_rows(const lsh::Fp8GemmArgs& g) { return g.M <= lsh::kSkMaxM; }
 
-// early_b: see Fp8SkinnyArgs.
-lsh_status fp8_gemm_launch(const lsh::Fp8GemmArgs& g, cudaStream_t st, int order = lsh::kF8Wait,
-                           int early_b = 0) {
-  if (fp8_few_rows(g))
-    return fp8_skinny_launch<lsh::kF8Store>(g, nullptr, nullptr, early_b, st);
+lsh_status fp8_gemm_launch(const lsh::Fp8GemmArgs& g, cudaStream_t st) {
+  if (fp8_few_rows(g)) return fp8_skinny_launch<lsh::kF8Store>(g, nullptr, nullptr, st);
   lsh::Fp8TcArgs a = {};
   a.g = g;
   a.wait_limit = g_wait_limit;
-  a.order = order;
   return g.b_rows == 1 ? fp8_tc_gemm<true>(a, st) : fp8_tc_gemm<false>(a, st);
 }
 
 // The hidden activation of the feed-forward: max(0, A B^T + bias) in 8 bits.
-lsh_status fp8_gemm_quant_launch(const lsh::Fp8GemmArgs& g, void* Q, float* qs, int order,
+lsh_status fp8_gemm_quant_launch(const lsh::Fp8GemmArgs& g, void* Q, float* qs,
                                  cudaStream_t st) {
-  if (fp8_few_rows(g)) return fp8_skinny_launch<lsh::kF8Quant>(g, Q, qs, 0, st);
+  if (fp8_few_rows(g)) return fp8_skinny_launch<lsh::kF8Quant>(g, Q, qs, st);
   lsh::Fp8TcArgs a = {};
   a.g = g;
   a.Q = static_cast<uint8_t*>(Q);
   a.qs = qs;
   a.wait_limit = g_wait_limit;
-  a.order = order;
   return fp8_pair_tiles(g) ? fp8_tc_launch<2, 256, lsh::kF8Quant, false, 1>(a, st)
                            : fp8_tc_launch<1, 128, lsh::kF8Quant, false, 1>(a, st);
 }
@@ -310,9 +303,8 @@ int64_t ffn8_step(int32_t tokens, int32_t d_ff, int32_t chunk) {
   return even < step ? even : step;
 }
 
-// Workspace of lsh_ffn_forward_fp8: the hidden activation of two steps, so
-// that one step's can be made while the last one's is still read (of one,
-// where there is no more).
+// Workspace of lsh_ffn_forward_fp8: the hidden activation of two steps, which
+// the steps use in turn (of one, where there is no more).
 struct Ffn8Layout {
   size_t h8[2], s[2], total;
 };
@@ -517,15 +509,9 @@ lsh_status lsh_ffn_forward_fp8(int32_t tokens, int32_t d_model, int32_t d_ff, in
   };
   const auto hidden = [&](int64_t c) { return w + l.h8[c & 1]; };
   const auto hidden_s = [&](int64_t c) { return reinterpret_cast<float*>(w + l.s[c & 1]); };
-  // up(c) makes chunk c's hidden activation, down(c) its output.  They go up(0),
-  // up(1), down(0), up(2), down(1), .., down(n - 1), so that each fills the SMs
-  // that the one before leaves idle at its end:
-  //   up(c + 1) loads inputs only; before its first store (into the buffer that
-  //   down(c - 1), just before it, reads) it waits for that grid, which had
-  //   itself waited for up(c) at its end; only then may down(c) start;
-  //   down(c) thus starts after up(c), and need not wait for up(c + 1).
-  // The last down has no up before it and waits at its start.  (A chunk of few
-  // rows takes the kernel for those, which always waits at its start.)
+  // up(c) makes chunk c's hidden activation, down(c) its output.  Each waits for
+  // the launch before it ahead of every load: a grid sees what another wrote
+  // only by a wait of its own, however the two are known to follow each other.
   const auto up = [&](int64_t c) {
     const int64_t c0 = c * step;
     lsh::Fp8GemmArgs g = fp8_gemm_args(rows_of(c), d_ff, d_model,
@@ -533,22 +519,17 @@ lsh_status lsh_ffn_forward_fp8(int32_t tokens, int32_t d_model, int32_t d_ff, in
                                        x_scales + c0 * kblocks(d_model), W1, w1_scales, 128);
     g.bias = static_cast<const __nv_bfloat16*>(b1);
     g.relu = 1;
-    return fp8_gemm_quant_launch(g, hidden(c), hidden_s(c), c ? lsh::kF8Late : lsh::kF8Wait, st);
+    return fp8_gemm_quant_launch(g, hidden(c), hidden_s(c), st);
   };
   const auto down = [&](int64_t c) {
     lsh::Fp8GemmArgs g = fp8_gemm_args(rows_of(c), d_model, d_ff, hidden(c), hidden_s(c), W2,
                                        w2_scales, 128);
     g.bias = static_cast<const __nv_bfloat16*>(b2);
     g.C = static_cast<__nv_bfloat16*>(Y) + c * step * d_model;
-    // W2 was complete before the first up's wait returned, and so before this
-    // launch can start
-    return fp8_gemm_launch(g, st, c + 1 < n_chunks ? lsh::kF8End : lsh::kF8Wait, 1);
+    return fp8_gemm_launch(g, st);
   };
-  if ((s = up(0)) != LSH_OK) return s;
-  for (int64_t c = 0; c < n_chunks; ++c) {
-    if (c + 1 < n_chunks && (s = up(c + 1)) != LSH_OK) return s;
-    if ((s = down(c)) != LSH_OK) return s;
-  }
+  for (int64_t c = 0; c < n_chunks; ++c)
+    if ((s = up(c)) != LSH_OK || (s = down(c)) != LSH_OK) return s;
   return LSH_OK;
 }
 

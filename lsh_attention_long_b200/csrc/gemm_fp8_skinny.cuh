@@ -30,9 +30,6 @@ struct Fp8SkinnyArgs {
   Fp8GemmArgs g;
   uint8_t* Q;   // kF8Quant, as in Fp8TcArgs
   float* qs;
-  // 1: B is not written by the previous grid in the stream, nor by any that
-  // may still run: its first loads need not wait for that grid
-  int early_b;
 };
 
 __device__ __forceinline__ void mma_sync_e4m3(float* c, uint32_t a0, uint32_t a1, uint32_t a2,
@@ -76,7 +73,6 @@ __global__ void __launch_bounds__(32 * kW) gemm_fp8_skinny_kernel(Fp8SkinnyArgs 
   const int n_c = (g.K + 127) >> 7;
   // shared memory of another CTA may be written only once that CTA has started
   if (kEpi == kF8Quant) tc::cluster_arrive_relaxed();
-  if (!a.early_b) grid_dep_wait();
   // a lane's own pieces [chunk in flight][row][half of the chunk]: nobody else
   // reads them, so the warps need no barrier
   extern __shared__ __align__(16) uint8_t ring[];
@@ -105,9 +101,22 @@ __global__ void __launch_bounds__(32 * kW) gemm_fp8_skinny_kernel(Fp8SkinnyArgs 
     }
     copy_commit();
   };
+  // Nothing is read before the grids before this one are done: B may be theirs.
+  // Its first pieces come as far as L2, where their writes go too, meanwhile.
+#pragma unroll
+  for (int d = 0; d < kSkDeep; ++d) {
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int k = (warp + kW * d) * 128 + 64 * half;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (pb[h] && k + 16 * tc4 < g.K)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(pb[h] + k) : "memory");
+    }
+  }
+  grid_dep_wait();
 #pragma unroll
   for (int d = 0; d < kSkDeep; ++d) fetch(warp + kW * d, d);
-  if (a.early_b) grid_dep_wait();
   struct Side {  // what a chunk needs of A, and the scales, a chunk ahead
     uint4 av[kNT][2];
     float sa[kNT][2], sb[2];

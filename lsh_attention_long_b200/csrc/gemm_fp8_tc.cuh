@@ -68,15 +68,7 @@ struct Fp8TcArgs {
   uint8_t* Q;      // kF8Quant: codes [M, N] of max(0, A B^T + bias)
   float* qs;       // and their 1 x 128 scales [M, ceil(N / 128)]
   long long wait_limit;
-  int order;  // Fp8Order
 };
-
-// How a grid follows the previous one in its stream (it may be scheduled while
-// that one finishes).  kF8Wait: waits for its end before any access.  The other
-// two load nothing that the previous grid writes, nor any that may still run.
-// kF8Late: waits before its first store, and only then lets the next grid
-// start.  kF8End: waits at its own end, so that this is the previous one's too.
-enum Fp8Order { kF8Wait = 0, kF8Late = 1, kF8End = 2 };
 
 template <int kPair, int kBN, int kEpi, bool kColScale>
 struct Fp8Cfg {
@@ -222,8 +214,8 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   else
     __syncthreads();
   tc::fence_after_sync();
-  if (a.order == kF8Wait) grid_dep_wait();
-  if (a.order != kF8Late) grid_dep_launch();
+  grid_dep_wait();
+  grid_dep_launch();
   const uint32_t tmem = S.tmem_base;
   const auto commit = [](uint64_t* bar) { kPair == 2 ? tc::mma_commit_pair(bar) : tc::mma_commit(bar); };
   const int n_n = (g.N + kBN - 1) / kBN;
@@ -492,10 +484,6 @@ __global__ void __launch_bounds__(kF8Threads, 1)
         __syncwarp();
         tc::mbar_arrive_if(tc::smem_u32(&S.sc_empty[slot]), lane == 0);  // its scales are read
       }
-      if (a.order == kF8Late && tile == 0) {
-        grid_dep_wait();
-        grid_dep_launch();
-      }
       // where the warps share barriers below, they all go on or none does
       const bool bad = kSplit || (kEpi == kF8Quant && kCols == 64)
                            ? f8_any(!ok)
@@ -629,8 +617,6 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     if (lane == 0) tc::bulk_wait();
     __syncwarp();
   }
-  // so that this grid's end is also the previous one's, whoever waits for it
-  if (a.order == kF8End) grid_dep_wait();
   if (kSplit && warp < 4) {  // the epilogue's two
     __syncwarp();
     tc::cluster_sync();

@@ -629,3 +629,69 @@ def test_pairs_of_ctas_that_leave_at_once(K, b_rows):
             L.lsh_matmul_fp8(A, sa, B, sb, out_dtype=F32, C=C)
         ok()
         assert all(torch.equal(C, first) for C in outs)
+
+
+@pytest.mark.parametrize("T,D,F,chunk", [(16000, 768, 8208, 128),   # pairs of CTAs throughout
+                                         (16000, 64, 8208, 128),    # the output on single ones
+                                         (645, 64, 131088, 128),    # the last step five positions
+                                         (13, 256, 1040, 128)])     # one step, few rows
+def test_feed_forward_of_what_was_written_just_before(T, D, F, chunk):
+    """Five steps whose input, weights, scales and biases were all rewritten in place right before
+    the call, by two sets in turn on the same buffers and workspace, eagerly and as a replayed
+    graph: the same bits as with a synchronisation after every launch sequence."""
+    g = gen(T + D)
+    sets = [[rnd(g, T, D) * (1 + 3 * i), rnd(g, F, D) / D ** 0.5, rnd(g, D, F) / F ** 0.5,
+             rnd(g, F, t=BF), rnd(g, D, t=BF)] for i in range(2)]
+    now = [t.clone() for t in sets[0]]
+    up128 = lambda n: ref.up(n, 128) // 128  # noqa: E731
+    e = lambda *sh, t=F32: torch.empty(*sh, dtype=t, device="cuda")  # noqa: E731
+    x8, sx = e(T, D, t=F8), e(T, up128(D))
+    w1, s1, w2, s2 = e(F, D, t=F8), e(up128(F), up128(D)), e(D, F, t=F8), e(up128(D), up128(F))
+    b1, b2 = e(F, t=BF), e(D, t=BF)
+    Y = e(T, D, t=BF)
+    ws = L.ffn_fp8_workspace(T, D, F, chunk, torch.device("cuda"))
+    ws.fill_(0x7f)  # NaN wherever something is read before it is written
+
+    def run(pause=lambda: None):
+        b1.copy_(now[3])
+        b2.copy_(now[4])
+        L.lsh_quantize_fp8(now[0], Y=x8, scales=sx)
+        L.lsh_quantize_fp8(now[1], block_rows=128, Y=w1, scales=s1)
+        L.lsh_quantize_fp8(now[2], block_rows=128, Y=w2, scales=s2)
+        pause()
+        L.lsh_ffn_forward_fp8(x8, sx, w1, s1, b1, w2, s2, b2, chunk, Y=Y, ws=ws)
+        pause()
+
+    def use(i):
+        for a, b in zip(now, sets[i]):
+            a.copy_(b)
+
+    want = []
+    for i in range(2):
+        use(i)
+        ok()
+        run(torch.cuda.synchronize)
+        want.append(Y.clone())
+    ok()
+    assert not torch.equal(*want) and not want[0].isnan().any()
+    got = []
+    for i in range(12):
+        use(i & 1)
+        run()
+        got.append(Y.clone())
+    ok()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for i in range(12):
+        use(i & 1)
+        graph.replay()
+        got.append(Y.clone())
+    ok()
+    assert all(torch.equal(y, want[i & 1]) for i, y in enumerate(got))
+    del graph
