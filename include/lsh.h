@@ -414,11 +414,12 @@ LSH_API lsh_status lsh_ffn_forward_fp8(int32_t tokens, int32_t d_model, int32_t 
  *                     feed-forward and 8-bit product kernels for the calls that
  *                     follow (not of the waits for what is in flight); 0
  *                     restores the default;
- *   hold_tile >= 0    in the calls that follow, the tensor-core attention
- *                     kernel's producers stop before tile `hold_tile` of each
- *                     thread block, so the waits for that tile's data run out
- *                     (their outputs are then undefined); -1 restores normal
- *                     operation.
+ *   hold_tile >= 0    in the calls that follow, the producers of the
+ *                     tensor-core attention kernel and of the 8-bit product
+ *                     kernel (more than 16 rows) stop before tile `hold_tile`
+ *                     of each thread block, so the waits for that tile's data
+ *                     run out (their outputs are then undefined); -1 restores
+ *                     normal operation.
  * The setting is process-wide and not synchronised with calls on other host
  * threads.  LSH_ERR_INVALID_ARG for wait_cycles < 0. */
 LSH_API lsh_status lsh_set_wait_test(int32_t hold_tile, int64_t wait_cycles);

@@ -242,6 +242,7 @@ lsh_status fp8_gemm_launch(const lsh::Fp8GemmArgs& g, cudaStream_t st) {
   lsh::Fp8TcArgs a = {};
   a.g = g;
   a.wait_limit = g_wait_limit;
+  a.hold_tile = g_hold_tile;
   return g.b_rows == 1 ? fp8_tc_gemm<true>(a, st) : fp8_tc_gemm<false>(a, st);
 }
 
@@ -254,6 +255,7 @@ lsh_status fp8_gemm_quant_launch(const lsh::Fp8GemmArgs& g, void* Q, float* qs,
   a.Q = static_cast<uint8_t*>(Q);
   a.qs = qs;
   a.wait_limit = g_wait_limit;
+  a.hold_tile = g_hold_tile;
   return fp8_pair_tiles(g) ? fp8_tc_launch<2, 256, lsh::kF8Quant, false, 1>(a, st)
                            : fp8_tc_launch<1, 128, lsh::kF8Quant, false, 1>(a, st);
 }

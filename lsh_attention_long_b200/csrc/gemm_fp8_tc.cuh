@@ -68,6 +68,7 @@ struct Fp8TcArgs {
   uint8_t* Q;      // kF8Quant: codes [M, N] of max(0, A B^T + bias)
   float* qs;       // and their 1 x 128 scales [M, ceil(N / 128)]
   long long wait_limit;
+  int hold_tile;   // test hook: the loads stop before this tile of each CTA (-1: never)
 };
 
 template <int kPair, int kBN, int kEpi, bool kColScale>
@@ -229,7 +230,9 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     // ------------------------------------------------------------ TMA loads
     if (lane == 0) {
       uint32_t q = 0;  // K blocks loaded
-      for (int u = first_unit; u < n_units && !*(volatile int*)&S.abort; u += unit_step) {
+      int tile = 0;
+      for (int u = first_unit; u < n_units && !*(volatile int*)&S.abort; u += unit_step, ++tile) {
+        if (tile == a.hold_tile) break;
         const int m0 = (u / n_n * kPair + rank) * kF8BM;
         const int n0 = (u % n_n) * kBN + (rank * (kBN / kPair));
         for (int kb = 0; kb < n_k; ++kb, ++q) {

@@ -491,8 +491,9 @@ def lsh_rev_backward(Y1, Y2, dY1, dY2, keys, perm, W1, b1, W2, b2, H: int, n_buc
 
 def lsh_set_wait_test(hold_tile: int = -1, wait_cycles: int = 0) -> None:
     """Test hook of the bounded device waits (see include/lsh.h): a clock-cycle
-    limit for the tensor-core attention kernel's waits (0 = default) and a tile
-    its producers withhold (-1 = none).  Process-wide."""
+    limit for the waits of the tensor-core attention, feed-forward and 8-bit
+    product kernels (0 = default) and a tile that the producers of attention and
+    8-bit products withhold (-1 = none).  Process-wide."""
     _call("lsh_set_wait_test", int(hold_tile), int(wait_cycles))
 
 

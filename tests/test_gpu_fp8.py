@@ -695,3 +695,61 @@ def test_feed_forward_of_what_was_written_just_before(T, D, F, chunk):
     ok()
     assert all(torch.equal(y, want[i & 1]) for i, y in enumerate(got))
     del graph
+
+
+def held(call, tile):
+    """The device status after `call` with tile `tile` of each block withheld and a short limit, and
+    the time until it was there."""
+    import time
+    L.lsh_set_wait_test(tile, 2_000_000)  # about 1 ms
+    try:
+        t0 = time.perf_counter()
+        call()
+        status = L.lsh_device_status()
+        return status, time.perf_counter() - t0
+    finally:
+        L.lsh_set_wait_test(-1, 0)
+
+
+@pytest.mark.parametrize("M,N,K,b_rows,tile", [
+    (128, 256, 1040, 128, 0), (1000, 656, 400, 1, 0),       # one CTA to a tile
+    (300, 640, 2064, 1, 0), (64, 512, 4096, 128, 0),        # clusters of 8 that share K
+    (64, 4096, 3088, 128, 0), (256, 4096, 4112, 1, 0),      # of 4 and 2
+    (2500, 1040, 400, 128, 0), (2500, 1040, 400, 1, 0),     # a pair
+    (40, 19200, 128, 128, 1), (8200, 1040, 144, 128, 1),    # its second tile
+    (8200, 1040, 2064, 1, 1)])
+def test_product_whose_loads_stop_is_reported_and_recovered(M, N, K, b_rows, tile):
+    g = gen(M + K)
+    A, sa = codes(g, M, K, 1)
+    B, sb = codes(g, N, K, b_rows)
+    want = L.lsh_matmul_fp8(A, sa, B, sb)
+    ok()
+    for _ in range(2):
+        status, seconds = held(lambda: L.lsh_matmul_fp8(A, sa, B, sb), tile)
+        assert status == 5 and seconds < 1.0  # LSH_ERR_TIMEOUT, by the short limit
+        assert torch.equal(L.lsh_matmul_fp8(A, sa, B, sb), want)
+        ok()
+
+
+@pytest.mark.parametrize("T,D,F,chunk", [(16000, 768, 8208, 128), (300, 144, 656, 256),
+                                         (2048, 768, 1024, 8192)])
+def test_feed_forward_whose_loads_stop_is_reported_and_recovered(T, D, F, chunk):
+    s = ffn_state(T, D, F)
+    want = ffn(s, chunk)
+    ok()
+    status, seconds = held(lambda: ffn(s, chunk), 0)
+    assert status == 5 and seconds < 1.0
+    assert torch.equal(ffn(s, chunk), want)
+    ok()
+
+
+def test_gradients_whose_loads_stop_are_reported_and_recovered():
+    g = gen(12)
+    dC, A = rnd(g, 1000, 656, t=BF), rnd(g, 1000, 400, t=BF)
+    _, _, Bt, st = L.lsh_quantize_fp8(rnd(g, 656, 400), block_rows=128, transposed=True)
+    want = L.lsh_matmul_fp8_backward(dC, A, Bt, st)
+    ok()
+    status, seconds = held(lambda: L.lsh_matmul_fp8_backward(dC, A, Bt, st), 0)
+    assert status == 5 and seconds < 1.0
+    assert all(torch.equal(a, b) for a, b in zip(L.lsh_matmul_fp8_backward(dC, A, Bt, st), want))
+    ok()
