@@ -29,10 +29,13 @@ __device__ __forceinline__ float relu_nan(float v) {
   return r;
 }
 
-// The codes of max(0, v[0 .. 3] * scale).
-__device__ __forceinline__ uint32_t e4m3x4_relu(const float* v, float scale) {
-  const float2 a = __fmul2_rn(make_float2(v[0], v[1]), make_float2(scale, scale));
-  const float2 b = __fmul2_rn(make_float2(v[2], v[3]), make_float2(scale, scale));
+// The codes of max(0, 448 v[0 .. 3] / m): s holds 448 / m as a sum of two
+// floats, and the quotient is rounded once.
+__device__ __forceinline__ uint32_t e4m3x4_relu(const float* v, const BlockScale& s) {
+  const float2 inv = make_float2(s.inv, s.inv), low = make_float2(s.lo, s.lo);
+  const float2 u = make_float2(v[0], v[1]), w = make_float2(v[2], v[3]);
+  const float2 a = __ffma2_rn(u, inv, __fmul2_rn(u, low));
+  const float2 b = __ffma2_rn(w, inv, __fmul2_rn(w, low));
   uint16_t lo, hi;
   asm("cvt.rn.satfinite.relu.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(a.y), "f"(a.x));
   asm("cvt.rn.satfinite.relu.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(b.y), "f"(b.x));

@@ -578,15 +578,16 @@ __global__ void __launch_bounds__(kF8Threads, 1)
           m = max(m, S.amax[half ^ 1][et]);
           asm volatile("bar.sync 1, 256;" ::: "memory");
         }
-        const float am = block_amax(m), inv = kE4m3Max / am;
+        const float am = block_amax(m);
+        const BlockScale sc(am);
         if (m0 + et < g.M && c0 < g.N && (c0 & 127) == 0)
           a.qs[(size_t)(m0 + et) * ((g.N + 127) >> 7) + (c0 >> 7)] = am / kE4m3Max;
         if (kCols == 128) wait_staging();
 #pragma unroll
         for (int p = 0; p < kCols / 16; ++p) {
           const float* v = acc + 16 * p;
-          const uint4 w = make_uint4(e4m3x4_relu(v, inv), e4m3x4_relu(v + 4, inv),
-                                     e4m3x4_relu(v + 8, inv), e4m3x4_relu(v + 12, inv));
+          const uint4 w = make_uint4(e4m3x4_relu(v, sc), e4m3x4_relu(v + 4, sc),
+                                     e4m3x4_relu(v + 8, sc), e4m3x4_relu(v + 12, sc));
           if (kCols == 128)
             *reinterpret_cast<uint4*>(my_row + ((p ^ swz) << 4)) = w;
           else if (m0 + et < g.M && c0 + 16 * p < g.N)  // two whole sectors of the row

@@ -753,3 +753,31 @@ def test_gradients_whose_loads_stop_are_reported_and_recovered():
     assert status == 5 and seconds < 1.0
     assert all(torch.equal(a, b) for a, b in zip(L.lsh_matmul_fp8_backward(dC, A, Bt, st), want))
     ok()
+
+
+@pytest.mark.parametrize("T,at_once", [(128, 1), (128, 7), (128, 16), (128, 128), (9600, 9600)])
+def test_feed_forward_quantises_as_defined_where_quotients_are_borders(T, at_once):
+    """Hidden entries M / 16 and M / 32, 128 <= M < 256, each such M being the largest of a block
+    once: many quotients 448 v / m lie exactly between two codes, and have to go to the even one.
+    W1 adds c and c' / 16 of two codes, which fp32 holds exactly; W2 hands the codes out."""
+    eye = torch.eye(128, device="cuda")
+    one = lambda *sh: torch.ones(*sh, device="cuda")  # noqa: E731
+    W1 = torch.cat([eye, eye / 16], 1).to(F8)          # [128, 256], scales 1
+    W2 = torch.cat([eye, torch.zeros_like(eye)]).to(F8)
+    big = (torch.arange(T, device="cuda") % 128 + 128).double()
+    M = (torch.arange(128, device="cuda") + 128).double().expand(T, 128).clone()
+    half = torch.full_like(M, 0.5)
+    M[:, 127], half[:, 127] = big, 1
+    c = torch.div(M, 16, rounding_mode="floor")
+    X = torch.cat([c * half, (M - 16 * c) * half], 1).to(F8)
+    h = M / 16 * half
+    q, s = ref.quantize(h)
+    z = lambda n: torch.zeros(n, dtype=BF, device="cuda")  # noqa: E731
+    for t in range(0, T, at_once):
+        x = X.view(torch.uint8)[t:t + at_once].view(F8)
+        Y = L.lsh_ffn_forward_fp8(x, one(len(x), 2), W1, one(1, 2), z(128), W2, one(2, 1), z(256),
+                                  128)
+        ok()
+        # Y is a code times its scale within 2^-8 + 2^-22, codes are 2^-4 apart or more
+        got = ref.round_e4m3(Y[:, :128].double() / s[t:t + at_once])
+        assert torch.equal(got, q[t:t + at_once]) and not Y[:, 128:].any()
