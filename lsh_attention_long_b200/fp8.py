@@ -32,15 +32,22 @@ def _up(n: int, to: int) -> int:
 
 
 def _fits(t, shape, dtype, index: int) -> bool:
-    """Whether t is None or a dense tensor of that shape and type on that device."""
-    return t is None or (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
-                         and t.get_device() == index and t.is_contiguous())
+    """Whether t is a dense tensor of that shape and type on that device."""
+    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.get_device() == index and t.is_contiguous())
 
 
-def _refuse(*specs):
+def _fits_if_given(t, shape, dtype, index: int) -> bool:
+    return t is None or _fits(t, shape, dtype, index)
+
+
+def _refuse(*specs, optional=()):
     """Reports what is wrong with (name, tensor, shape, dtype) entries, of
-    which one at least does not fit."""
-    _validate([(n, t, s, d, True) for n, t, s, d in specs])
+    which one at least does not fit (those of ``optional`` may be None)."""
+    for name, t, _, _ in specs:
+        if t is None:
+            raise TypeError(f"{name} must be a torch.Tensor")
+    _validate([(n, t, s, d, True) for n, t, s, d in (*specs, *optional)])
     raise ValueError("tensors must be on one CUDA device")
 
 
@@ -146,11 +153,11 @@ def lsh_rmsnorm_forward(X, w, *, R=None, eps: float = 1e-6, out_dtype=None, H=No
     if not fits:
         _refuse(("X", X, shape, X.dtype),
                 ("w", w, (cols,), w.dtype),
-                ("R", R, shape, rt),
-                ("H", H, shape, X.dtype),
-                ("Y", Y, shape, yt),
-                ("scales", scales, (rows, _up(cols, 128) // 128), f32),
-                ("rstd", rstd, (rows,), f32))
+                optional=(("R", R, shape, rt),
+                          ("H", H, shape, X.dtype),
+                          ("Y", Y, shape, yt),
+                          ("scales", scales, (rows, _up(cols, 128) // 128), f32),
+                          ("rstd", rstd, (rows,), f32)))
     with _on(dev, stream):
         if R is not None and H is None:
             H = torch.empty_like(X)
@@ -183,16 +190,16 @@ def lsh_rmsnorm_backward(dY, H, w, rstd, *, dH=None, dX=None, dw=None, ws=None, 
             and _fits(H, shape, H.dtype, dev)
             and _fits(w, (cols,), w.dtype, dev)
             and _fits(rstd, (rows,), f32, dev)
-            and _fits(dH, shape, H.dtype, dev)
-            and _fits(dX, shape, H.dtype, dev)
-            and _fits(dw, (cols,), f32, dev)):
+            and _fits_if_given(dH, shape, H.dtype, dev)
+            and _fits_if_given(dX, shape, H.dtype, dev)
+            and _fits_if_given(dw, (cols,), f32, dev)):
         _refuse(("dY", dY, shape, dY.dtype),
                 ("H", H, shape, H.dtype),
                 ("w", w, (cols,), w.dtype),
                 ("rstd", rstd, (rows,), f32),
-                ("dH", dH, shape, H.dtype),
-                ("dX", dX, shape, H.dtype),
-                ("dw", dw, (cols,), f32))
+                optional=(("dH", dH, shape, H.dtype),
+                          ("dX", dX, shape, H.dtype),
+                          ("dw", dw, (cols,), f32)))
     with _on(dev, stream):
         if dX is None:
             dX = torch.empty_like(H)
@@ -223,15 +230,15 @@ def lsh_quantize_fp8(X, *, block_rows: int = 1, transposed: bool = False, Y=None
     dev = _device(X, "X")
     if dev < 0 or not (
             _fits(X, (rows, cols), X.dtype, dev)
-            and _fits(Y, (rows, cols), F8, dev)
-            and _fits(scales, s_shape, f32, dev)
-            and _fits(Yt, yt_shape, F8, dev)
-            and _fits(scales_t, t_shape, f32, dev)):
+            and _fits_if_given(Y, (rows, cols), F8, dev)
+            and _fits_if_given(scales, s_shape, f32, dev)
+            and _fits_if_given(Yt, yt_shape, F8, dev)
+            and _fits_if_given(scales_t, t_shape, f32, dev)):
         _refuse(("X", X, (rows, cols), X.dtype),
-                ("Y", Y, (rows, cols), F8),
-                ("scales", scales, s_shape, f32),
-                ("Yt", Yt, yt_shape, F8),
-                ("scales_t", scales_t, t_shape, f32))
+                optional=(("Y", Y, (rows, cols), F8),
+                          ("scales", scales, s_shape, f32),
+                          ("Yt", Yt, yt_shape, F8),
+                          ("scales_t", scales_t, t_shape, f32)))
     with _on(dev, stream):
         if Y is None:
             Y = torch.empty_like(X, dtype=F8)
@@ -281,8 +288,8 @@ def lsh_matmul_fp8(A, a_scales, B, b_scales, *, bias=None, relu: bool = False,
                 ("a_scales", a_scales, (M, kb), f32),
                 ("B", B, (N, K), F8),
                 ("b_scales", b_scales, sb_shape, f32),
-                ("bias", bias, (N,), torch.bfloat16),
-                ("C", C, (M, N), out_dtype))
+                optional=(("bias", bias, (N,), torch.bfloat16),
+                          ("C", C, (M, N), out_dtype)))
     with _on(dev, stream):
         if C is None:
             C = A.new_empty((M, N), dtype=out_dtype)
@@ -309,16 +316,16 @@ def lsh_matmul_fp8_backward(dC, A, Bt, bt_scales, *, out_dtype=torch.bfloat16, d
             and _fits(A, (M, K), bf, dev)
             and _fits(Bt, (K, N), F8, dev)
             and _fits(bt_scales, (_up(K, 128) // 128, _up(N, 128) // 128), f32, dev)
-            and _fits(dA, (M, K), out_dtype, dev)
-            and _fits(dB, (N, K), f32, dev)
-            and _fits(db, (N,), f32, dev)):
+            and _fits_if_given(dA, (M, K), out_dtype, dev)
+            and _fits_if_given(dB, (N, K), f32, dev)
+            and _fits_if_given(db, (N,), f32, dev)):
         _refuse(("dC", dC, (M, N), bf),
                 ("A", A, (M, K), bf),
                 ("Bt", Bt, (K, N), F8),
                 ("bt_scales", bt_scales, (_up(K, 128) // 128, _up(N, 128) // 128), f32),
-                ("dA", dA, (M, K), out_dtype),
-                ("dB", dB, (N, K), f32),
-                ("db", db, (N,), f32))
+                optional=(("dA", dA, (M, K), out_dtype),
+                          ("dB", dB, (N, K), f32),
+                          ("db", db, (N,), f32)))
     with _on(dev, stream):
         if dA is None:
             dA = torch.empty_like(A, dtype=out_dtype)
@@ -335,7 +342,8 @@ def lsh_matmul_fp8_backward(dC, A, Bt, bt_scales, *, out_dtype=torch.bfloat16, d
 
 
 def ffn_fp8_workspace(tokens: int, d_model: int, d_ff: int, chunk: int, device) -> torch.Tensor:
-    """Device scratch for lsh_ffn_forward_fp8: the hidden activation of two chunks."""
+    """Device scratch for lsh_ffn_forward_fp8: the hidden activation of two times ``chunk``
+    positions, or of as many as take 32 MB each where that is more (and no more than there are)."""
     n = load_library().lsh_ffn_fp8_ws_size(tokens, d_model, d_ff, chunk)
     return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
 
@@ -383,7 +391,7 @@ def lsh_ffn_forward_fp8(X, x_scales, W1, w1_scales, b1, W2, w2_scales, b2, chunk
                 ("W2", W2, (d_model, d_ff), F8),
                 ("w2_scales", w2_scales, (mb, fb), f32),
                 ("b2", b2, (d_model,), bf),
-                ("Y", Y, X.shape, bf))
+                optional=(("Y", Y, X.shape, bf),))
     with _on(dev, stream):
         if Y is None:
             Y = torch.empty_like(X, dtype=bf)

@@ -79,6 +79,54 @@ def test_feed_forward_binding():
         L.lsh_ffn_forward_fp8(X, s, W1, one, b1.float(), W2, one, b2, 128)
 
 
+def test_a_missing_tensor_is_named():
+    """None where a tensor is needed (the norm gives no rstd unless asked) is refused by name."""
+    X, w, A, Bm, s = z(4, 64), z(64), z(4, 256, t=F8), z(32, 256, t=F8), z(4, 2)
+    dC, Ab, Bt = z(4, 32, t=BF), z(4, 256, t=BF), z(256, 32, t=F8)
+    X8, W1, W2 = z(4, 64, t=F8), z(128, 64, t=F8), z(64, 128, t=F8)
+    one, b1, b2 = z(1, 1), z(128, t=BF), z(64, t=BF)
+    layer = [X8, z(4, 1), W1, one, b1, W2, one, b2]
+    calls = [("rstd", lambda: L.lsh_rmsnorm_backward(X, X, w, None)),
+             ("a_scales", lambda: L.lsh_matmul_fp8(A, None, Bm, z(1, 2))),
+             ("b_scales", lambda: L.lsh_matmul_fp8(A, s, Bm, None)),
+             ("Bt", lambda: L.lsh_matmul_fp8_backward(dC, Ab, None, z(2, 1))),
+             ("bt_scales", lambda: L.lsh_matmul_fp8_backward(dC, Ab, Bt, None))]
+    for i, name in enumerate(("x_scales", "W1", "w1_scales", "b1", "W2", "w2_scales", "b2"), 1):
+        args = layer[:i] + [None] + layer[i + 1:]
+        calls.append((name, lambda a=args: L.lsh_ffn_forward_fp8(*a, 128)))
+    for name, call in calls:
+        with pytest.raises(TypeError, match=f"^{name} must be a torch.Tensor"):
+            call()
+    for name, call in (("X", lambda: L.lsh_rmsnorm_forward(None, w)),
+                       ("w", lambda: L.lsh_rmsnorm_forward(X, None)),
+                       ("dY", lambda: L.lsh_rmsnorm_backward(None, X, w, z(4))),
+                       ("H", lambda: L.lsh_rmsnorm_backward(X, None, w, z(4))),
+                       ("X", lambda: L.lsh_quantize_fp8(None)),
+                       ("B", lambda: L.lsh_matmul_fp8(A, s, None, s)),
+                       ("X", lambda: L.lsh_ffn_forward_fp8(None, *layer[1:], 128))):
+        with pytest.raises(ValueError, match=f"^{name} must be"):
+            call()
+
+
+def test_a_missing_tensor_is_named_on_the_device_too(monkeypatch):
+    """The same where everything else fits: the library is not reached."""
+    from lsh_attention_long_b200 import fp8
+
+    class OnDevice(torch.Tensor):
+        get_device = lambda self: 0  # noqa: E731
+        is_cuda = property(lambda self: True)
+
+    d = lambda *sh, t=F32: z(*sh, t=t).as_subclass(OnDevice)  # noqa: E731
+    monkeypatch.setattr(fp8, "_lib", lambda: pytest.fail("reached the library"))
+    for name, call in (("rstd", lambda: L.lsh_rmsnorm_backward(d(4, 64), d(4, 64), d(64), None)),
+                       ("Bt", lambda: L.lsh_matmul_fp8_backward(d(4, 32, t=BF), d(4, 256, t=BF),
+                                                                None, d(2, 1))),
+                       ("bt_scales", lambda: L.lsh_matmul_fp8_backward(
+                           d(4, 32, t=BF), d(4, 256, t=BF), d(256, 32, t=F8), None))):
+        with pytest.raises(TypeError, match=f"^{name} must be a torch.Tensor"):
+            call()
+
+
 @pytest.fixture(scope="module")
 def lib():
     B.build()
