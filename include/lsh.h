@@ -322,7 +322,8 @@ LSH_API lsh_status lsh_rev_backward(const lsh_shape* shape, int32_t d_ff, int32_
  * block that holds an infinity or a NaN stands for NaN throughout.
  *
  * All sizes called cols, N, K, d_model and d_ff are multiples of 16
- * (else LSH_ERR_UNSUPPORTED); numbers of rows, M and tokens are any.  The
+ * (else LSH_ERR_UNSUPPORTED); numbers of rows, M and tokens are any.  M, N, K,
+ * tokens, d_model, d_ff and the quantiser's cols are at most 2^31 - 256.  The
  * kernels run on the current device, which must be the buffers' own.
  * Every call is asynchronous on `stream`, allocates nothing, keeps nothing
  * between calls and gives the same bits for the same inputs. */

@@ -19,6 +19,9 @@ inline size_t kblocks(int cols) { return (size_t)((cols + 127) / 128); }
 // multiples of 16
 inline size_t pitch16(int rows) { return ((size_t)rows + 15) & ~(size_t)15; }
 
+// Sizes that a kernel rounds up to whole tiles and indexes with 32 bits.
+constexpr int32_t kFp8MaxSize = 0x7fffffff - 255;
+
 lsh_status norm_check(int32_t rows, int32_t cols) {
   if (rows < 0 || cols <= 0) return LSH_ERR_INVALID_ARG;
   if (cols % 16 || cols > lsh::kNormMaxCols) return LSH_ERR_UNSUPPORTED;
@@ -123,7 +126,8 @@ lsh::QuantArgs quant_args(int32_t rows, int32_t cols, const void* X, void* Y, fl
 
 lsh_status fp8_sizes_check(int32_t M, int32_t N, int32_t K) {
   if (M < 0 || N <= 0 || K <= 0) return LSH_ERR_INVALID_ARG;
-  if (N % 16 || K % 16) return LSH_ERR_UNSUPPORTED;
+  if (N % 16 || K % 16 || M > kFp8MaxSize || N > kFp8MaxSize || K > kFp8MaxSize)
+    return LSH_ERR_UNSUPPORTED;
   return LSH_OK;
 }
 
@@ -330,7 +334,9 @@ Ffn8Layout ffn8_layout(int32_t tokens, int32_t d_ff, int32_t chunk) {
 
 lsh_status ffn8_check(int32_t tokens, int32_t d_model, int32_t d_ff, int32_t chunk) {
   if (tokens < 0 || d_model <= 0 || d_ff <= 0 || chunk <= 0) return LSH_ERR_INVALID_ARG;
-  if (d_model % 16 || d_ff % 16 || chunk % 128) return LSH_ERR_UNSUPPORTED;
+  if (d_model % 16 || d_ff % 16 || chunk % 128 || tokens > kFp8MaxSize ||
+      d_model > kFp8MaxSize || d_ff > kFp8MaxSize)
+    return LSH_ERR_UNSUPPORTED;
   return LSH_OK;
 }
 
@@ -401,7 +407,7 @@ lsh_status lsh_quantize_fp8(int32_t rows, int32_t cols, int32_t x_dtype, int32_t
                             void* stream) {
   if (!is_f32_or_bf16(x_dtype) || rows < 0 || cols <= 0 || (block_rows != 1 && block_rows != 128))
     return LSH_ERR_INVALID_ARG;
-  if (cols % 16) return LSH_ERR_UNSUPPORTED;
+  if (cols % 16 || cols > kFp8MaxSize) return LSH_ERR_UNSUPPORTED;
   if (rows == 0) return LSH_OK;
   if (!X || (!Y && !Yt) || (Y && !scales) || (Yt && !scales_t)) return LSH_ERR_INVALID_ARG;
   if (any_misaligned({X, Y, scales, Yt, scales_t})) return LSH_ERR_INVALID_ARG;

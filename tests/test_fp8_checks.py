@@ -208,3 +208,20 @@ def test_feed_forward_abi(lib):
     # a longer chunk asked for: two of it, and no more than the positions there are
     assert size(1 << 25, 64, 128, 1 << 20) >= 2 * 128 << 20
     assert size(1000, 64, 128, 1 << 20) < 1 << 18
+
+
+def test_sizes_beyond_whole_tiles_of_32_bits(lib):
+    """Sizes whose tiles end past 2^31 are refused, not wrapped round."""
+    for n in (2 ** 31 - 16, 2 ** 31 - 240):
+        for M, N, K in ((n, 16, 16), (1, n, 16), (1, 16, n)):
+            assert lib.lsh_matmul_fp8(M, N, K, P, P, P, P, 128, None, 0, 1, P, None) == UNSUPPORTED
+            assert lib.lsh_matmul_fp8_bwd_ws_size(M, N, K) == 0
+            assert lib.lsh_matmul_fp8_backward(M, N, K, P, P, P, P, 1, P, P, P, P, 1 << 62,
+                                               None) == UNSUPPORTED
+        assert lib.lsh_quantize_fp8(1, n, 1, 1, P, P, P, None, None, None) == UNSUPPORTED
+        for T, D, F in ((n, 16, 16), (1, n, 16), (1, 16, n)):
+            assert lib.lsh_ffn_fp8_ws_size(T, D, F, 128) == 0
+            assert lib.lsh_ffn_forward_fp8(T, D, F, 128, *[P] * 10, 1 << 62, None) == UNSUPPORTED
+    n = 2 ** 31 - 256
+    assert lib.lsh_matmul_fp8_bwd_ws_size(n, 16, 16) > 4 * n
+    assert lib.lsh_ffn_fp8_ws_size(n, 16, 16, 128) >= 32 << 20
