@@ -781,3 +781,62 @@ def test_feed_forward_quantises_as_defined_where_quotients_are_borders(T, at_onc
         # Y is a code times its scale within 2^-8 + 2^-22, codes are 2^-4 apart or more
         got = ref.round_e4m3(Y[:, :128].double() / s[t:t + at_once])
         assert torch.equal(got, q[t:t + at_once]) and not Y[:, 128:].any()
+
+
+def near_borders(g, rows, cols):
+    """fp32 entries whose quotients 448 v / m are a few units of their last place from a border
+    between two codes, m being each 1 x 128 block's first entry and all of its column's."""
+    m = (1 + torch.rand(cols // 128, generator=g)).repeat_interleave(128).expand(rows, cols)
+    c = torch.randint(16, 32, (rows, cols), generator=g) | 1          # borders: odd, of five bits
+    c = c * 2.0 ** torch.randint(-4, 4, (rows, cols), generator=g)    # 1 to 248
+    v = (c.double() * m / 448).float()
+    v = v.view(torch.int32) + torch.randint(-2, 3, (rows, cols), generator=g).int()
+    v = v.view(torch.float32)
+    v[:, ::128] = m[:, ::128]
+    return torch.where(torch.rand(rows, cols, generator=g) < 0.5, v, -v).contiguous()
+
+
+def off_by(quot, codes, d):
+    """Codes that no quotient within d of the exact one (relative) has."""
+    lo, hi = ref.round_e4m3(quot * (1 - d)), ref.round_e4m3(quot * (1 + d))
+    return int(((codes != lo) & (codes != hi)).sum())
+
+
+# the quotient to the last bit of an fp32: half a unit, and what the sum that is rounded once is
+# off by itself, far below 2^-10 of that
+ONCE = 2.0 ** -24 * (1 + 2.0 ** -10)
+
+
+@pytest.mark.parametrize("block_rows", [1, 128])
+@pytest.mark.parametrize("rows", [3, 640])
+def test_quantize_fp32_next_to_borders(rows, block_rows):
+    """Quotients are right to the last bit of an fp32; the product with a rounded inverse, the mistake
+    planted in the oracle, is not."""
+    cols = 1024
+    host = near_borders(torch.Generator().manual_seed(rows), rows, cols)
+    quot, s = ref.blocks(host.double(), block_rows)
+    m = ref.expand(s, block_rows, rows, cols) * 448
+    assert off_by(quot, ref.round_e4m3(quot.float().double()), ONCE) == 0
+    assert off_by(quot, ref.round_e4m3((host * (448 / m.float())).double()), ONCE) > rows
+    X = host.cuda()
+    Y, S, Yt, St = L.lsh_quantize_fp8(X, block_rows=block_rows, transposed=True)
+    Y1, S1 = L.lsh_quantize_fp8(X, block_rows=block_rows)
+    ok()
+    assert torch.equal(Y.view(torch.uint8), Y1.view(torch.uint8)) and torch.equal(S, S1)
+    assert off_by(quot.cuda(), Y.double(), ONCE) == 0
+    t = torch.nn.functional.pad(host.t().double(), (0, ref.up(rows, 16) - rows))
+    assert off_by(ref.blocks(t, block_rows)[0].cuda(), Yt.double(), ONCE) == 0
+
+
+@pytest.mark.parametrize("cols", [1024, 4096])
+def test_norm_codes_next_to_borders(cols):
+    """The norm's codes are those of its own fp32 output, quotients right to the last bit."""
+    g = torch.Generator().manual_seed(cols)
+    X = torch.randn(40, cols, generator=g).cuda()
+    w = near_borders(g, 1, cols)[0].cuda() / X[0]
+    _, y, _, _ = L.lsh_rmsnorm_forward(X, w)
+    _, Y, S, _ = L.lsh_rmsnorm_forward(X, w, out_dtype=F8)
+    ok()
+    quot, s = ref.blocks(y.double(), 1)
+    assert off_by(quot, Y.double(), ONCE) == 0
+    close(S, s, 2.0 ** -24 * s)  # one division
