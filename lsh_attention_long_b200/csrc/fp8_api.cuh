@@ -202,11 +202,13 @@ lsh_status fp8_skinny_launch(const lsh::Fp8SkinnyArgs& a, cudaStream_t st) {
   return fp8_skinny_launch<kNT, 8, kEpi>(a, st);
 }
 template <int kEpi>
-lsh_status fp8_skinny_launch(const lsh::Fp8GemmArgs& g, void* Q, float* qs, cudaStream_t st) {
+lsh_status fp8_skinny_launch(const lsh::Fp8GemmArgs& g, void* Q, float* qs, cudaStream_t st,
+                             int prefetch_b = 0) {
   lsh::Fp8SkinnyArgs a = {};
   a.g = g;
   a.Q = static_cast<uint8_t*>(Q);
   a.qs = qs;
+  a.prefetch_b = prefetch_b;
   return g.M <= 8 ? fp8_skinny_launch<1, kEpi>(a, st) : fp8_skinny_launch<2, kEpi>(a, st);
 }
 
@@ -241,8 +243,9 @@ lsh_status fp8_tc_gemm(const lsh::Fp8TcArgs& a, cudaStream_t st) {
 
 bool fp8_few_rows(const lsh::Fp8GemmArgs& g) { return g.M <= lsh::kSkMaxM; }
 
-lsh_status fp8_gemm_launch(const lsh::Fp8GemmArgs& g, cudaStream_t st) {
-  if (fp8_few_rows(g)) return fp8_skinny_launch<lsh::kF8Store>(g, nullptr, nullptr, st);
+// prefetch_b: see Fp8SkinnyArgs.
+lsh_status fp8_gemm_launch(const lsh::Fp8GemmArgs& g, cudaStream_t st, int prefetch_b = 0) {
+  if (fp8_few_rows(g)) return fp8_skinny_launch<lsh::kF8Store>(g, nullptr, nullptr, st, prefetch_b);
   lsh::Fp8TcArgs a = {};
   a.g = g;
   a.wait_limit = g_wait_limit;
@@ -534,7 +537,7 @@ lsh_status lsh_ffn_forward_fp8(int32_t tokens, int32_t d_model, int32_t d_ff, in
                                        w2_scales, 128);
     g.bias = static_cast<const __nv_bfloat16*>(b2);
     g.C = static_cast<__nv_bfloat16*>(Y) + c * step * d_model;
-    return fp8_gemm_launch(g, st);
+    return fp8_gemm_launch(g, st, 1);
   };
   for (int64_t c = 0; c < n_chunks; ++c)
     if ((s = up(c)) != LSH_OK || (s = down(c)) != LSH_OK) return s;

@@ -30,6 +30,7 @@ struct Fp8SkinnyArgs {
   Fp8GemmArgs g;
   uint8_t* Q;   // kF8Quant, as in Fp8TcArgs
   float* qs;
+  int prefetch_b;  // 1: B's first pieces go to L2 while the previous grid ends
 };
 
 __device__ __forceinline__ void mma_sync_e4m3(float* c, uint32_t a0, uint32_t a1, uint32_t a2,
@@ -101,17 +102,19 @@ __global__ void __launch_bounds__(32 * kW) gemm_fp8_skinny_kernel(Fp8SkinnyArgs 
     }
     copy_commit();
   };
-  // Nothing is read before the grids before this one are done: B may be theirs.
-  // Its first pieces come as far as L2, where their writes go too, meanwhile.
+  // Nothing is read before the grids before this one are done, since B may be
+  // theirs; a prefetch to L2, where their writes go too, is no read.
+  if (a.prefetch_b) {
 #pragma unroll
-  for (int d = 0; d < kSkDeep; ++d) {
+    for (int d = 0; d < kSkDeep; ++d) {
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int k = (warp + kW * d) * 128 + 64 * half;
+      for (int half = 0; half < 2; ++half) {
+        const int k = (warp + kW * d) * 128 + 64 * half;
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        if (pb[h] && k + 16 * tc4 < g.K)
-          asm volatile("prefetch.global.L2 [%0];" ::"l"(pb[h] + k) : "memory");
+        for (int h = 0; h < 2; ++h)
+          if (pb[h] && k + 16 * tc4 < g.K)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(pb[h] + k) : "memory");
+      }
     }
   }
   grid_dep_wait();
