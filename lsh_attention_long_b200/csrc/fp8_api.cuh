@@ -163,7 +163,8 @@ lsh_status fp8_tc_launch(const lsh::Fp8TcArgs& a, cudaStream_t st) {
     return LSH_ERR_CUDA;
   constexpr size_t smem = lsh::fp8_tc_smem_bytes<kPair, kBN, kEpi, kColScale>();
   const auto kernel = lsh::gemm_fp8_tc_kernel<kPair, kBN, kEpi, kColScale, kParts>;
-  // the kernel's register split adds up only if it was built with kF8Regs
+  // the kernel's register split adds up only if it was built with kF8Regs, which
+  // a compiler other than the one it was written with might not give it
   static const bool regs_ok = [&] {
     cudaFuncAttributes at;
     return cudaFuncGetAttributes(&at, kernel) == cudaSuccess && at.numRegs == lsh::kF8Regs;
@@ -301,7 +302,8 @@ Fp8BwdLayout fp8_bwd_layout(int32_t M, int32_t N, int32_t K) {
 // Positions that lsh_ffn_forward_fp8 takes at a time: `chunk`, or more where their
 // hidden activation stays within kFfn8Hidden bytes (two chunks' then take half
 // of the L2, and every product is a launch: 65 536 positions, 512 -> 2048 ->
-// 512, take 227 us by 8192 and 200 by 16 384), in parts of nearly equal size.
+// 512, took 227 us by 8192 and 202 by 16 384, 199 now), in parts of nearly equal
+// size.
 constexpr size_t kFfn8Hidden = (size_t)32 << 20;
 int64_t ffn8_step(int32_t tokens, int32_t d_ff, int32_t chunk) {
   const int64_t fit = (int64_t)(kFfn8Hidden / (size_t)d_ff) / 256 * 256;

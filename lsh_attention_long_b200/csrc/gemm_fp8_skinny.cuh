@@ -8,9 +8,9 @@
 // brings for itself, already in the fragment layout of mma.sync m16n8k32 (B's
 // rows are its 16 rows, A's rows its 8 columns): a piece serves two MMAs, with
 // the codes of K taken in the same permuted order from both operands.  (One row:
-// 8192 x 2048 6.1 us, 16 384 x 8192 27 us, 4.9 TB/s; with loads into registers,
+// 8192 x 2048 5.9 us, 16 384 x 8192 27 us, 4.9 TB/s; with loads into registers,
 // which wait between batches, 6.7 and 39; these and codes converted to fp16
-// first, m16n8k16, 8.9 and 53.  16 rows: 7.9 and 35 us, tcgen05 tiles 8.8 and
+// first, m16n8k16, 8.9 and 53.  16 rows: 7.5 and 36 us, tcgen05 tiles 8.8 and
 // 39.)
 //
 // A block of kW warps has 16 rows of B; its warps share out K in chunks of 128,

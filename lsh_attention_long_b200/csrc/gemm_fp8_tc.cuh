@@ -16,10 +16,14 @@
 // CTAs of a cluster share out a tile's K and add their totals up through
 // distributed shared memory.
 //
-// Measured: 8192 x 4096 x 4096 in 120 us (2 270 TFLOP/s, 61% of the tensor
-// cores' cycles; with column scales 167 us).  What is left is the exchange of
-// the two accumulators: each is written in 512 cycles, handed over in some 370
-// (commit, arrival, next issue) and read and added in 360 at best.
+// Measured: 8192 x 4096 x 4096 in 120 us over twenty warm calls (2 280 TFLOP/s,
+// 60% of the tensor cores' cycles; with column scales 169 us), 134 and 190 us
+// where the board's power sets the clock.  The busiest pair takes 837 cycles a
+// block, of which 512 are its MMAs'; the epilogue with neither loads nor MMAs
+// took 795, so it sets the pace.  Its parts measured alone do not add up to
+// that: reading and adding 360 at best, and some 370 from commit to the next
+// issue, would be 621 a block with two accumulators in turn.  (The forms on
+// pairs spill 72 to 88 bytes a thread.)
 //
 // Warp roles (384 threads, persistent blocks, one per SM):
 //   warp 0      one thread loads A and B tiles of 128-byte rows with TMA

@@ -6,9 +6,11 @@
 //
 // One pass over the data: a row stays in registers between the sum of its
 // squares and the scaling, so each input is read and each output written
-// once, and the kernels are bound by memory (65 536 x 512, fp32 stream and bf16
-// residual to 8 bits: 58 us, 6.4 TB/s; gradients of 16 384 x 2048 fp32: 75 us,
-// 6.3 TB/s).  Rows of up to 1024 columns are
+// once, and the kernels are bound by memory (in a graph of such calls, 65 536 x
+// 512, fp32 stream and bf16 residual to 8 bits: 58 us, 6.4 TB/s; gradients of
+// 16 384 x 2048 fp32: 77 us, 6.1 TB/s), but for the gradients of rows of more
+// than 8192 columns, whose registers spill (4096 x 16 384: 960 us fp32, 800
+// bf16, of 143 and 82 that memory would take).  Rows of up to 1024 columns are
 // a warp's (no barrier), longer ones a block's of 256 to 1024 threads (with 256
 // threads for all of them, 4096 x 8192 bf16 took 1.3 times as long); a thread
 // holds kNV pieces of 8 consecutive columns, piece t + i * kT, so that 16

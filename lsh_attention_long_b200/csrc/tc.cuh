@@ -296,8 +296,11 @@ __device__ __forceinline__ uint32_t cluster_map(uint32_t saddr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
   return r;
 }
-// An arrival that publishes no memory writes (the caller's reads are done): a
-// release at cluster scope took over a thousand cycles.
+// An arrival that publishes no memory writes: what it tells is that the caller's
+// reads of tensor memory are done, and those have reached its registers when
+// tcgen05.wait::ld returns, before this is issued (a tcgen05.fence orders the
+// two).  A release at cluster scope, which would wait for the caller's stores as
+// well, took over a thousand cycles.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr, bool pred) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
