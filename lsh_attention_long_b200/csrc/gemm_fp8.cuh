@@ -29,8 +29,23 @@ __device__ __forceinline__ float relu_nan(float v) {
   return r;
 }
 
-// The codes of max(0, 448 v[0 .. 3] / m): s holds 448 / m as a sum of two
-// floats, and the quotient is rounded once.
+// 448 / m as a sum of two floats for the two functions below.  The second is
+// above zero, so that an entry of -inf stays one (-inf * 0, or the sum of two
+// infinities, would be NaN); the smallest float in place of a zero is far below
+// half of the first's last place.
+__device__ __forceinline__ BlockScale relu_scale(float am) {
+  float inv = kE4m3Max / am, rest = fmaf(-inv, am, kE4m3Max);
+  if (rest < 0.f) {  // rounded up: the next smaller float
+    inv = __uint_as_float(__float_as_uint(inv) - 1);
+    rest = fmaf(-inv, am, kE4m3Max);
+  }
+  return BlockScale(inv, fmaxf(rest * inv * (1.f / kE4m3Max), __uint_as_float(1u)));
+}
+// 448 v / m, rounded once.
+__device__ __forceinline__ float scaled(float v, const BlockScale& s) {
+  return fmaf(v, s.inv, v * s.lo);
+}
+// The codes of max(0, 448 v[0 .. 3] / m).
 __device__ __forceinline__ uint32_t e4m3x4_relu(const float* v, const BlockScale& s) {
   const float2 inv = make_float2(s.inv, s.inv), low = make_float2(s.lo, s.lo);
   const float2 u = make_float2(v[0], v[1]), w = make_float2(v[2], v[3]);

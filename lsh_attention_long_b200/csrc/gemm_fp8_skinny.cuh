@@ -234,9 +234,8 @@ __global__ void __launch_bounds__(32 * kW) gemm_fp8_skinny_kernel(Fp8SkinnyArgs 
 #pragma unroll
       for (int c = 0; c < kCluster; ++c) b = max(b, __float_as_uint(cmax[c][m]));
       const float am = block_amax(b);
-      const BlockScale sc(am);
-      a.Q[(size_t)m * g.N + n] = (uint8_t)__nv_cvt_float_to_fp8(
-          fmaf(v[i], sc.inv, v[i] * sc.lo), __NV_SATFINITE, __NV_E4M3);
+      a.Q[(size_t)m * g.N + n] =
+          (uint8_t)__nv_cvt_float_to_fp8(scaled(v[i], relu_scale(am)), __NV_SATFINITE, __NV_E4M3);
       if ((n & 127) == 0) a.qs[(size_t)m * ((g.N + 127) >> 7) + (n >> 7)] = am / kE4m3Max;
     }
   }

@@ -583,7 +583,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
           asm volatile("bar.sync 1, 256;" ::: "memory");
         }
         const float am = block_amax(m);
-        const BlockScale sc(am);
+        const BlockScale sc = relu_scale(am);
         if (m0 + et < g.M && c0 < g.N && (c0 & 127) == 0)
           a.qs[(size_t)(m0 + et) * ((g.N + 127) >> 7) + (c0 >> 7)] = am / kE4m3Max;
         if (kCols == 128) wait_staging();

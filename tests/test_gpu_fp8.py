@@ -840,3 +840,31 @@ def test_norm_codes_next_to_borders(cols):
     quot, s = ref.blocks(y.double(), 1)
     assert off_by(quot, Y.double(), ONCE) == 0
     close(S, s, 2.0 ** -24 * s)  # one division
+
+
+@pytest.mark.parametrize("T,D,F", [(3, 256, 512), (16, 256, 512), (40, 256, 512), (2500, 256, 1040)])
+def test_feed_forward_of_units_switched_off(T, D, F):
+    """A bias of -inf switches a hidden unit off: max(0, -inf) is 0, whatever its block's largest
+    entry.  The same bits as with a bias of -1e30, which does so as well."""
+    s = ffn_state(T, D, F)
+    off = torch.rand(F, generator=gen(1), device="cuda") < 0.3
+    off[128:256] = True                                # a block of zeros
+    s["b1"][:16] = torch.tensor([7, 14, 28, 1.75] * 4, device="cuda")  # blocks whose largest entry divides 448
+    s["b1"][16:128] = 1
+    s["W1"].view(torch.uint8)[:128] = 0
+    off[:128:3] = True
+    want = ffn(dict(s, b1=torch.where(off, -1e30, s["b1"].float()).to(BF)), 128)
+    got = ffn(dict(s, b1=torch.where(off, -float("inf"), s["b1"].float()).to(BF)), 128)
+    ok()
+    assert not want.isnan().any() and torch.equal(got, want)
+    # as numbers: what a 64-bit sum over the units that are left gives, within the codes' steps
+    h = ref.values(s["X8"], s["sx"]) @ ref.values(s["W1"], s["s1"], 128).t() + s["b1"].double()
+    h = h.clamp_min(0) * ~off
+    W2 = ref.values(s["W2"], s["s2"], 128)
+    exact = h @ W2.t() + s["b2"].double()
+    top = torch.nn.functional.pad(h, (0, ref.up(F, 128) - F)).view(T, -1, 128).amax(2)
+    # half a step of a code (2^-4 of the entry, or 2^-10 scales), the fp32 sums before it
+    # moving an entry by far less than that again, and the output's rounding
+    step = torch.maximum(h * 2.0 ** -4, ref.expand(top / 448, 1, T, F) * 2.0 ** -10)
+    tol = 1.01 * (step @ W2.abs().t()) + 1e-3
+    close(got, exact, tol + HALF[BF] * (exact.abs() + tol))
